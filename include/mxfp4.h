@@ -286,6 +286,178 @@ mx_status mx_gemm_f8_tw(int transA, int transB, int64_t M, int64_t N, int64_t K,
                         mx_layout layout, mx_dtype out_dtype,
                         void *C, int64_t ldc, hipStream_t stream);
 
+/*
+ * ---- Layers of experts: rows grouped by expert ----
+ * A routed linear layer keeps one weight per expert and multiplies each row
+ * with the weight of the expert it was routed to, the rows sorted by expert.
+ * The groups are given by `group_ends`: device int32[groups], the cumulative
+ * end positions; group e is rows [group_ends[e-1], group_ends[e]) of the M
+ * grouped rows (from 0 for e = 0), possibly none.  The ends are read by the
+ * kernels, never by the host, so a router's output needs no synchronization
+ * and a captured graph may be replayed with other ends.  Values are clamped
+ * to [0, M], a value below its predecessor counts as the predecessor.  Rows
+ * behind the last group belong to none.
+ *
+ * Grouped blobs (MX_LAYOUT_TILED): the parts of the groups one behind the
+ * other, each exactly the tiled blob that mx_quantize_dual gives for the
+ * group's n_e rows alone:
+ *   row-wise:    rows n_e, length N; group e starts after sum_{j<e}
+ *                cdiv(n_j,16)*16 blob rows;
+ *   column-wise: rows N, length n_e; its data starts after sum_{j<e}
+ *                cdiv(n_j,128) atoms of each of the cdiv(N,16) row groups, its
+ *                scales after sum_{j<e} cdiv(n_j,512) scale atoms of each.
+ * Bytes behind the last group's part are not written.
+ * The weights of the experts (groups of equally many rows, E x N x K as one
+ * (E*N) x K tensor with ends N, 2N, ...) are quantized the same way: the
+ * row-wise blob is the forward product's B, the column-wise one dgrad's.
+ */
+
+/*
+ * Bytes that the grouped blobs of M rows of N elements need at most, whatever
+ * the ends are.  Each output pointer may be NULL.
+ * Errors: MX_ERR_INVALID_ARGUMENT (negative size, groups < 1).
+ */
+mx_status mx_grouped_blob_bytes(int64_t M, int64_t N, int groups, size_t *row_data_bytes, size_t *row_scale_bytes,
+                                size_t *col_data_bytes, size_t *col_scale_bytes);
+
+/*
+ * Grouped MXFP4 quantization: the row-wise grouped blob and, when q_col /
+ * s_col are given, the column-wise one from the same read of x (q_col = s_col
+ * = NULL: row-wise only, as serving needs).
+ *   row_index: NULL: grouped row r is row r of x (x_rows must be >= M).
+ *     Otherwise device int32[M]: grouped row r is row row_index[r] of x (the
+ *     rows of a token routed to several experts are gathered in the same
+ *     read); an index outside [0, x_rows) gives a row of zeros.
+ *   x: x_rows x N bf16, stride ldx.  Options as mx_quantize_dual (NULL = all
+ *     zero); the element index of stochastic rounding is index_base + r*N + j
+ *     with the grouped row r.
+ *   layout: MX_LAYOUT_TILED.
+ * Rows in no group are not read.  M == 0 or N == 0 is a no-op.
+ * Requires x and the outputs 16-byte aligned, ldx % 8 == 0, group_ends and
+ * row_index 4-byte aligned, and M < 2^30.
+ * Errors: INVALID_ARGUMENT, MISALIGNED, UNSUPPORTED (layout, options, M),
+ * DEVICE_UNSUPPORTED, HIP.
+ */
+mx_status mx_quantize_grouped(const void *x, int64_t x_rows, int64_t N, int64_t ldx, const int32_t *row_index,
+                              int64_t M, const int32_t *group_ends, int groups, const mx_quant_opts *row_opts,
+                              const mx_quant_opts *col_opts, mx_layout layout, void *q_row, void *s_row,
+                              void *q_col, void *s_col, hipStream_t stream);
+
+/*
+ * Grouped product, forward and dgrad of a layer of experts:
+ *   C[r][j] = sum_k A[r][k] * B_e[j][k] (+ bias[e][j])   for the rows r of group e
+ * A: a row-wise grouped blob of M rows along K.  B: `groups` tiled blobs of N
+ * rows along K, one behind the other (the row-wise grouped blob of weights
+ * for forward, the column-wise one for dgrad).  C: M x N, stride ldc, in the
+ * grouped order; rows in no group are written as 0.  bias: NULL, or groups x
+ * N bf16 values (2-byte aligned), added before the one rounding to out_dtype.
+ * The matrix instruction, its accumulation and rounding as mx_gemm_a4w4;
+ * K == 0 writes the bias, or zeros.  M == 0 or N == 0 is a no-op.
+ * Requires 16-byte aligned operands and C, ldc % 8 == 0.  M rows of A and one
+ * group of B must each stay below 2 GiB of blob data.
+ * Errors: INVALID_ARGUMENT, MISALIGNED, UNSUPPORTED (layout, out_dtype, sizes),
+ * DEVICE_UNSUPPORTED, HIP.
+ */
+mx_status mx_gemm_a4w4_grouped(int64_t M, int64_t N, int64_t K, const int32_t *group_ends, int groups,
+                               const void *A, const void *A_scale, const void *B, const void *B_scale,
+                               mx_layout layout, mx_dtype out_dtype, const void *bias, void *C, int64_t ldc,
+                               hipStream_t stream);
+
+/*
+ * Grouped wgrad of a layer of experts: for each group e
+ *   C_e[i][j] = sum_r A[i][r] * B[j][r]   over the group's rows r  (i < N, j < K)
+ * A: the column-wise grouped blob of the output gradient (M rows of N), B:
+ * the column-wise grouped blob of the input (M rows of K), both with the same
+ * ends.  C_e: N x K with row stride ldc at C + e * group_stride elements; a
+ * group without rows is written as 0.
+ * Requires 16-byte aligned operands and C, ldc % 8 == 0, group_stride % 8 == 0
+ * and group_stride >= N * ldc unless groups == 1.  Each blob must stay below
+ * 2 GiB of data.
+ * Errors as mx_gemm_a4w4_grouped.  N == 0 or K == 0 is a no-op.
+ */
+mx_status mx_gemm_a4w4_grouped_wgrad(int64_t M, int64_t N, int64_t K, const int32_t *group_ends, int groups,
+                                     const void *A, const void *A_scale, const void *B, const void *B_scale,
+                                     mx_layout layout, mx_dtype out_dtype, void *C, int64_t ldc,
+                                     int64_t group_stride, hipStream_t stream);
+
+/*
+ * ---- AdamW over many tensors ----
+ * One step of AdamW (Loshchilov and Hutter, decoupled weight decay) for every
+ * tensor of a table.  Per element, in fp32 with each operation rounded by
+ * itself:
+ *   g = grad * grad_scale;  m = beta1*m + (1-beta1)*g;  v = beta2*v + (1-beta2)*(g*g)
+ *   param = param*decay - (m / (sqrt(v)*root_factor + eps)) * step_size
+ * with decay = 1 - lr*weight_decay, step_size = lr / (1 - beta1^step),
+ * root_factor = 1 / sqrt(1 - beta2^step), each rounded once from double.
+ *
+ * States (MX_STATE_*): fp32, or MXFP8: 32 consecutive elements share an E8M0
+ * scale byte c (2^(c-127), 0xFF = NaN block) and each is an OCP E4M3 code; m
+ * is held as such, v as its square root.  c is the smallest that keeps the
+ * block's largest magnitude within 448: c = max(exponent field of amax - 8 +
+ * (mantissa above 1.75), 0).  Codes round to nearest even, or, with use_sr,
+ * stochastically: element n draws the word n%4 of Philox-4x32-10 with counter
+ * (lo32(n>>2), hi32(n>>2), tensor_id, 4) and key = seed, its low 16 bits for m,
+ * its high 16 bits for sqrt(v); with F = the 16 bits that follow the code's
+ * bits in the magnitude's binary expansion, it rounds up iff the bits + F
+ * carry.  A positive sqrt(v) never becomes code 0.  A block that holds Inf or
+ * NaN gets scale 0xFF and zero codes.  Zero bytes are the initial states.
+ */
+typedef enum mx_state_dtype {
+    MX_STATE_F32 = 0,
+    MX_STATE_MXFP8 = 1
+} mx_state_dtype;
+
+/* What changes from step to step. */
+typedef struct mx_adamw_step {
+    float grad_scale;    /* multiplies the gradient (1 / loss scale, clipping) */
+    float decay;
+    float step_size;
+    float root_factor;
+    uint64_t seed;       /* of stochastic rounding: another one each step */
+} mx_adamw_step;
+
+typedef struct mx_adamw_tensor {
+    void *param;           /* numel of param_dtype, updated in place */
+    const void *grad;      /* numel of grad_dtype */
+    void *exp_avg;         /* m: numel fp32, or numel E4M3 bytes */
+    void *exp_avg_sq;      /* v: numel fp32, or numel E4M3 bytes of sqrt(v) */
+    void *exp_avg_scale;   /* MXFP8: cdiv(numel,32) bytes each (any alignment); else NULL */
+    void *exp_avg_sq_scale;
+    void *param_copy;      /* NULL, or numel bf16: the updated parameter, nearest even */
+    int64_t numel;
+    uint32_t tensor_id;
+} mx_adamw_tensor;
+
+typedef struct mx_adamw_opts {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;          /* counted from 1 */
+    double grad_scale;
+    uint64_t seed;
+    int param_dtype;       /* MX_F32 or MX_BF16 (rounded to nearest even) */
+    int grad_dtype;        /* MX_F32 or MX_BF16 */
+    int state_dtype;       /* mx_state_dtype */
+    uint32_t use_sr;       /* MXFP8 states: stochastic rounding */
+    /* NULL, or a device mx_adamw_step that replaces the values computed from
+     * lr, weight_decay, step, grad_scale and seed: a captured graph is replayed
+     * with new values in it, and a clipping factor needs no host round trip. */
+    const mx_adamw_step *device_step;
+} mx_adamw_opts;
+
+/* The step values of opts, as mx_adamw uses them.  Errors: MX_ERR_INVALID_ARGUMENT. */
+mx_status mx_adamw_step_values(const mx_adamw_opts *opts, mx_adamw_step *step);
+
+/*
+ * One step over tensors[0..count) (a host array, read before the call
+ * returns).  Tensors with numel == 0 are skipped; no two tensors may overlap.
+ * One launch for up to 48 tensors.
+ * Requires param, grad, states and param_copy 16-byte aligned.
+ * Errors: MX_ERR_INVALID_ARGUMENT (NULL, count < 0, numel < 0, betas outside
+ * [0, 1), eps < 0, step < 1, use_sr not 0 or 1, non-finite values),
+ * MX_ERR_MISALIGNED, MX_ERR_UNSUPPORTED (a dtype, numel above 2^33, a bf16
+ * copy of bf16 parameters), MX_ERR_DEVICE_UNSUPPORTED, MX_ERR_HIP.
+ */
+mx_status mx_adamw(const mx_adamw_tensor *tensors, int64_t count, const mx_adamw_opts *opts, hipStream_t stream);
+
 /* ------------------------------------------------------------------ MXFP6
  *
  * MXFP6: the same 32-element blocks and E8M0 scales with 6-bit elements.

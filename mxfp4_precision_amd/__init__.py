@@ -34,11 +34,15 @@ MX_BF16 = 0
 MX_F32 = 1
 MX_FP6_E2M3 = 2
 MX_FP6_E3M2 = 3
+MX_STATE_F32 = 0
+MX_STATE_MXFP8 = 1
 
 EXPORTED = ("mx_blob_bytes", "mx_quantize_rowwise", "mx_quantize_dual", "mx_gemm_a4w4", "mx_gemm_a4w4_bias",
             "mx_layout_convert", "mx_layout_convert_host", "mx_dequantize", "mx_device_supported",
             "mx_fp8_blob_bytes", "mx_quantize_fp8_tw", "mx_gemm_f8_tw",
             "mx_fp6_blob_bytes", "mx_quantize_fp6", "mx_gemm_fp6", "mx_quantize_dual_mul",
+            "mx_grouped_blob_bytes", "mx_quantize_grouped", "mx_gemm_a4w4_grouped", "mx_gemm_a4w4_grouped_wgrad",
+            "mx_adamw", "mx_adamw_step_values",
             "mx_measure_mfma", "mx_set_device_arch_override", "mx_status_string", "mx_last_error")
 
 
@@ -57,6 +61,47 @@ class mx_quant_opts(ctypes.Structure):
 def quant_opts(use_2d_block: bool = False, use_sr: bool = False, seed: int = 0,
                tensor_id: int = 0, index_base: int = 0, rht: int = 0) -> mx_quant_opts:
     return mx_quant_opts(int(use_2d_block), int(use_sr), seed, tensor_id, index_base, rht)
+
+
+class mx_adamw_step(ctypes.Structure):
+    _fields_ = [("grad_scale", ctypes.c_float), ("decay", ctypes.c_float), ("step_size", ctypes.c_float),
+                ("root_factor", ctypes.c_float), ("seed", ctypes.c_uint64)]
+
+
+class mx_adamw_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("param_copy", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("tensor_id", ctypes.c_uint32)]
+
+
+class mx_adamw_opts(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
+                ("grad_scale", ctypes.c_double), ("seed", ctypes.c_uint64), ("param_dtype", ctypes.c_int),
+                ("grad_dtype", ctypes.c_int), ("state_dtype", ctypes.c_int), ("use_sr", ctypes.c_uint32),
+                ("device_step", ctypes.c_void_p)]
+
+
+def adamw_opts(lr: float, step: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+               weight_decay: float = 0.0, grad_scale: float = 1.0, seed: int = 0, param_dtype: int = MX_F32,
+               grad_dtype: int = MX_BF16, state_dtype: int = MX_STATE_F32, use_sr: bool = False,
+               device_step=None) -> mx_adamw_opts:
+    """device_step: a GPU tensor that holds an mx_adamw_step (24 bytes); the caller keeps it alive."""
+    return mx_adamw_opts(lr, beta1, beta2, eps, weight_decay, step, grad_scale, seed, param_dtype, grad_dtype,
+                         state_dtype, int(use_sr), _dptr(device_step))
+
+
+def adamw_tensor(param, grad, exp_avg, exp_avg_sq, numel: int, exp_avg_scale=None, exp_avg_sq_scale=None,
+                 param_copy=None, tensor_id: int = 0) -> mx_adamw_tensor:
+    """One row of an mx_adamw table.  It holds addresses: the caller keeps the tensors alive."""
+    return mx_adamw_tensor(_dptr(param), _dptr(grad), _dptr(exp_avg), _dptr(exp_avg_sq), _dptr(exp_avg_scale),
+                           _dptr(exp_avg_sq_scale), _dptr(param_copy), numel, tensor_id)
+
+
+def adamw_table(rows):
+    """The host array of mx_adamw (built once, used every step while the addresses stay)."""
+    return (mx_adamw_tensor * max(len(rows), 1))(*rows)
 
 
 _lib = None
@@ -87,6 +132,13 @@ def lib() -> ctypes.CDLL:
     L.mx_quantize_fp6.argtypes = [vp, i64, i64, i64, i32, optp, i32, optp, i32, vp, vp, vp, vp, vp]
     L.mx_quantize_dual_mul.argtypes = [vp, vp, i64, i64, i64, i64, optp, optp, i32, vp, vp, vp, vp, vp]
     L.mx_gemm_fp6.argtypes = [i32, i32, i64, i64, i64, i32, vp, vp, i32, vp, vp, i32, i32, vp, i64, vp]
+    szp = ctypes.POINTER(ctypes.c_size_t)
+    L.mx_grouped_blob_bytes.argtypes = [i64, i64, i32, szp, szp, szp, szp]
+    L.mx_quantize_grouped.argtypes = [vp, i64, i64, i64, vp, i64, vp, i32, optp, optp, i32, vp, vp, vp, vp, vp]
+    L.mx_gemm_a4w4_grouped.argtypes = [i64, i64, i64, vp, i32, vp, vp, vp, vp, i32, i32, vp, vp, i64, vp]
+    L.mx_gemm_a4w4_grouped_wgrad.argtypes = [i64, i64, i64, vp, i32, vp, vp, vp, vp, i32, i32, vp, i64, i64, vp]
+    L.mx_adamw.argtypes = [ctypes.POINTER(mx_adamw_tensor), i64, ctypes.POINTER(mx_adamw_opts), vp]
+    L.mx_adamw_step_values.argtypes = [ctypes.POINTER(mx_adamw_opts), ctypes.POINTER(mx_adamw_step)]
     L.mx_dequantize.argtypes = [vp, vp, i64, i64, i32, vp, i64, vp]
     L.mx_measure_mfma.argtypes = [i32, i32, vp, i32, i64, vp, vp]
     L.mx_set_device_arch_override.argtypes = [ctypes.c_char_p]
@@ -126,6 +178,16 @@ def _dptr(p) -> Optional[int]:
             raise TypeError("a device pointer is required, got a tensor on %s" % p.device)
         return p.data_ptr()
     raise TypeError("a device pointer is required, got %r (host arrays are not accepted)" % type(p))
+
+
+def _i32ptr(p, count: int) -> Optional[int]:
+    """A device pointer to `count` int32 values.  A tensor of another type, with gaps or with fewer values is
+    refused: the kernels read that many consecutive 32-bit words."""
+    if hasattr(p, "data_ptr"):
+        if str(p.dtype) != "torch.int32" or not p.is_contiguous() or p.numel() < count:
+            raise TypeError("a contiguous int32 tensor of at least %d values is required, got %s of %s"
+                            % (count, p.dtype, tuple(p.shape)))
+    return _dptr(p)
 
 
 def _hptr(p) -> Optional[int]:
@@ -228,6 +290,47 @@ def mx_gemm_f8_tw(transA: int, transB: int, M: int, N: int, K: int, A, a_scale_i
                                _dptr(b_scale_inv), layout, out_dtype, _dptr(C), ldc, _stream(stream)))
 
 
+def mx_grouped_blob_bytes(M: int, N: int, groups: int) -> Tuple[int, int, int, int]:
+    """(row data, row scales, column data, column scales): the most bytes that M rows in `groups` groups need."""
+    n = [ctypes.c_size_t() for _ in range(4)]
+    _check(lib().mx_grouped_blob_bytes(M, N, groups, *(ctypes.byref(v) for v in n)))
+    return tuple(v.value for v in n)
+
+
+def mx_quantize_grouped(x, x_rows: int, N: int, ldx: int, row_index, M: int, group_ends, groups: int, row_opts,
+                        col_opts, layout: int, q_row, s_row, q_col=None, s_col=None, stream=None):
+    _check(lib().mx_quantize_grouped(_dptr(x), x_rows, N, ldx, _i32ptr(row_index, M), M, _i32ptr(group_ends, groups), groups,
+                                     _opts(row_opts), _opts(col_opts), layout, _dptr(q_row), _dptr(s_row),
+                                     _dptr(q_col), _dptr(s_col), _stream(stream)))
+
+
+def mx_gemm_a4w4_grouped(M: int, N: int, K: int, group_ends, groups: int, A, A_scale, B, B_scale, layout: int,
+                         out_dtype: int, bias, C, ldc: int, stream=None):
+    _check(lib().mx_gemm_a4w4_grouped(M, N, K, _i32ptr(group_ends, groups), groups, _dptr(A), _dptr(A_scale), _dptr(B),
+                                      _dptr(B_scale), layout, out_dtype, _dptr(bias), _dptr(C), ldc,
+                                      _stream(stream)))
+
+
+def mx_gemm_a4w4_grouped_wgrad(M: int, N: int, K: int, group_ends, groups: int, A, A_scale, B, B_scale, layout: int,
+                               out_dtype: int, C, ldc: int, group_stride: int, stream=None):
+    _check(lib().mx_gemm_a4w4_grouped_wgrad(M, N, K, _i32ptr(group_ends, groups), groups, _dptr(A), _dptr(A_scale), _dptr(B),
+                                            _dptr(B_scale), layout, out_dtype, _dptr(C), ldc, group_stride,
+                                            _stream(stream)))
+
+
+def mx_adamw(tensors, count: int, opts: mx_adamw_opts, stream=None):
+    """tensors: an array of adamw_table.  count may not exceed its length."""
+    if tensors is not None and count > len(tensors):
+        raise ValueError("count=%d, but the table holds %d tensors" % (count, len(tensors)))
+    _check(lib().mx_adamw(tensors, count, ctypes.byref(opts), _stream(stream)))
+
+
+def mx_adamw_step_values(opts: mx_adamw_opts) -> mx_adamw_step:
+    step = mx_adamw_step()
+    _check(lib().mx_adamw_step_values(ctypes.byref(opts), ctypes.byref(step)))
+    return step
+
+
 def mx_layout_convert(to_tiled: int, rows: int, length: int, q_src, s_src, q_dst, s_dst, stream=None):
     _check(lib().mx_layout_convert(to_tiled, rows, length, _dptr(q_src), _dptr(s_src), _dptr(q_dst),
                                    _dptr(s_dst), _stream(stream)))
@@ -272,3 +375,10 @@ def empty_blob(rows: int, length: int, layout: int, device="cuda"):
     db, sb = mx_blob_bytes(rows, length, layout)
     return (torch.empty(max(db, 1), dtype=torch.uint8, device=device),
             torch.empty(max(sb, 1), dtype=torch.uint8, device=device))
+
+
+def empty_grouped_blob(M: int, N: int, groups: int, device="cuda"):
+    """Allocate (row data, row scales, column data, column scales) uint8 tensors for any split of M rows of N
+    elements into `groups` groups."""
+    import torch
+    return tuple(torch.empty(max(n, 1), dtype=torch.uint8, device=device) for n in mx_grouped_blob_bytes(M, N, groups))

@@ -15,8 +15,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmxfp4.so")
-SOURCES = ["api.cpp", "layout.cpp", "quantize.hip", "quantize_fp8.hip", "gemm.hip", "convert.hip",
-           "dequantize.hip", "measure.hip"]
+SOURCES = ["api.cpp", "layout.cpp", "quantize.hip", "quantize_fp8.hip", "gemm.hip", "gemm_grouped.hip",
+           "adamw.hip", "convert.hip", "dequantize.hip", "measure.hip"]
 ARCH = "gfx950"
 
 

@@ -5,6 +5,7 @@
 // for the same reason: silent fallbacks hid wrong layouts and lost speed).
 
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -426,6 +427,246 @@ mx_status mx_gemm_f8_tw(int transA, int transB, int64_t M, int64_t N, int64_t K,
                                             static_cast<const uint8_t *>(B), b_scale_inv, out_dtype, C, ldc,
                                             stream),
                         "mx_gemm_f8_tw");
+}
+
+namespace {
+
+constexpr int64_t kMaxGroupedRows = int64_t(1) << 30;   // row and unit counts are 32-bit in the kernels
+
+mx_status check_groups(int64_t M, const int32_t *group_ends, int groups) {
+    if (M < 0) return fail(MX_ERR_INVALID_ARGUMENT, "negative row count M=%lld", (long long)M);
+    if (groups < 1) return fail(MX_ERR_INVALID_ARGUMENT, "groups=%d must be >= 1", groups);
+    if (!group_ends) return fail(MX_ERR_INVALID_ARGUMENT, "group_ends is NULL");
+    if (reinterpret_cast<uintptr_t>(group_ends) & 3u)
+        return fail(MX_ERR_MISALIGNED, "group_ends must be 4-byte aligned");
+    if (M >= kMaxGroupedRows || groups >= kMaxGroupedRows)
+        return fail(MX_ERR_UNSUPPORTED, "M=%lld rows in %d groups: both must stay below 2^30", (long long)M, groups);
+    return MX_SUCCESS;
+}
+
+// What the two grouped products check alike.
+mx_status check_grouped_gemm(const char *name, int64_t M, int64_t N, int64_t K, const int32_t *group_ends, int groups,
+                             const void *A, const void *A_scale, const void *B, const void *B_scale, mx_layout layout,
+                             mx_dtype out_dtype, const void *C, int64_t ldc, int64_t columns, bool need_operands) {
+    if (N < 0 || K < 0)
+        return fail(MX_ERR_INVALID_ARGUMENT, "negative shape N=%lld K=%lld", (long long)N, (long long)K);
+    MX_TRY(check_groups(M, group_ends, groups));
+    MX_TRY(check_layout(layout));
+    if (layout != MX_LAYOUT_TILED) return fail(MX_ERR_UNSUPPORTED, "%s reads MX_LAYOUT_TILED blobs only", name);
+    if (out_dtype != MX_BF16 && out_dtype != MX_F32)
+        return fail(MX_ERR_UNSUPPORTED, "out_dtype %d (valid: MX_BF16=0, MX_F32=1)", (int)out_dtype);
+    if (ldc < columns || ldc < 1)
+        return fail(MX_ERR_INVALID_ARGUMENT, "ldc=%lld must be >= max(%lld, 1)", (long long)ldc, (long long)columns);
+    if (!C) return fail(MX_ERR_INVALID_ARGUMENT, "C is NULL");
+    if (need_operands && (!A || !A_scale || !B || !B_scale))
+        return fail(MX_ERR_INVALID_ARGUMENT, "operand pointer is NULL");
+    if (!aligned16(C) ||
+        (need_operands && (!aligned16(A) || !aligned16(A_scale) || !aligned16(B) || !aligned16(B_scale))))
+        return fail(MX_ERR_MISALIGNED, "operands and C must be 16-byte aligned");
+    if (ldc % 8) return fail(MX_ERR_MISALIGNED, "ldc=%lld must be a multiple of 8", (long long)ldc);
+    if (N >= kMaxGroupedRows || K >= kMaxGroupedRows)
+        return fail(MX_ERR_UNSUPPORTED, "N=%lld and K=%lld must stay below 2^30", (long long)N, (long long)K);
+    return MX_SUCCESS;
+}
+
+}  // namespace
+
+mx_status mx_grouped_blob_bytes(int64_t M, int64_t N, int groups, size_t *row_data_bytes, size_t *row_scale_bytes,
+                                size_t *col_data_bytes, size_t *col_scale_bytes) {
+    if (M < 0 || N < 0) return fail(MX_ERR_INVALID_ARGUMENT, "negative blob shape");
+    if (groups < 1) return fail(MX_ERR_INVALID_ARGUMENT, "groups=%d must be >= 1", groups);
+    // the most units of `per` rows that M rows in at most min(groups, M) groups with rows fill
+    const int64_t full = groups < M ? groups : M;
+    const auto most = [&](int64_t per) { return (M + (per - 1) * full) / per; };
+    const int64_t n16 = mx::cdiv(N, 16) * 16, Np = mx::padded(N);
+    if (row_data_bytes) *row_data_bytes = (size_t)(most(16) * 16 * (Np / 2));
+    if (row_scale_bytes) *row_scale_bytes = (size_t)(most(16) * 16 * (mx::cdiv(Np, 512) * 16));
+    if (col_data_bytes) *col_data_bytes = (size_t)(most(128) * 64 * n16);
+    if (col_scale_bytes) *col_scale_bytes = (size_t)(most(512) * 16 * n16);
+    return MX_SUCCESS;
+}
+
+mx_status mx_quantize_grouped(const void *x, int64_t x_rows, int64_t N, int64_t ldx, const int32_t *row_index,
+                              int64_t M, const int32_t *group_ends, int groups, const mx_quant_opts *row_opts,
+                              const mx_quant_opts *col_opts, mx_layout layout, void *q_row, void *s_row, void *q_col,
+                              void *s_col, hipStream_t stream) {
+    const bool dual = q_col || s_col;
+    MX_TRY(validate_x(x, x_rows, N, ldx));
+    MX_TRY(check_groups(M, group_ends, groups));
+    if (!row_index && x_rows < M)
+        return fail(MX_ERR_INVALID_ARGUMENT, "x has %lld rows, fewer than M=%lld (no row_index)", (long long)x_rows,
+                    (long long)M);
+    if (reinterpret_cast<uintptr_t>(row_index) & 3u)
+        return fail(MX_ERR_MISALIGNED, "row_index must be 4-byte aligned");
+    MX_TRY(check_opts(row_opts, "row"));
+    if (dual) MX_TRY(check_opts(col_opts, "col"));
+    MX_TRY(check_layout(layout));
+    if (layout != MX_LAYOUT_TILED) return fail(MX_ERR_UNSUPPORTED, "mx_quantize_grouped writes MX_LAYOUT_TILED blobs only");
+    MX_TRY(validate_out(q_row, s_row, "row-wise"));
+    if (dual) MX_TRY(validate_out(q_col, s_col, "column-wise"));
+    if (M == 0 || N == 0) return MX_SUCCESS;
+    MX_TRY(check_device());
+    mx::QuantArgs a{};
+    a.x = static_cast<const uint16_t *>(x);
+    a.M = M; a.N = N; a.ldx = ldx;
+    a.N_pad = mx::padded(N);
+    a.row = to_dir(row_opts);
+    if (dual) a.col = to_dir(col_opts);
+    a.sr_pairs = (dual && N % 16 == 0 && a.row.index_base % 16 == 0 && a.col.index_base % 16 == 0) ? 1u : 0u;
+    a.q_row = static_cast<uint8_t *>(q_row);
+    a.s_row = static_cast<uint8_t *>(s_row);
+    a.q_col = static_cast<uint8_t *>(q_col);
+    a.s_col = static_cast<uint8_t *>(s_col);
+    a.ends = group_ends;
+    a.row_index = row_index;
+    a.groups = groups;
+    a.x_rows = x_rows;
+    return check_launch(mx::launch_quantize_grouped(a, dual, stream), "mx_quantize_grouped");
+}
+
+mx_status mx_gemm_a4w4_grouped(int64_t M, int64_t N, int64_t K, const int32_t *group_ends, int groups, const void *A,
+                               const void *A_scale, const void *B, const void *B_scale, mx_layout layout,
+                               mx_dtype out_dtype, const void *bias, void *C, int64_t ldc, hipStream_t stream) {
+    const char *name = "mx_gemm_a4w4_grouped";
+    MX_TRY(check_grouped_gemm(name, M, N, K, group_ends, groups, A, A_scale, B, B_scale, layout, out_dtype, C, ldc, N,
+                              K > 0));
+    if (reinterpret_cast<uintptr_t>(bias) & 1u) return fail(MX_ERR_MISALIGNED, "bias must be 2-byte aligned");
+    MX_TRY(check_blob_limit(name, "A", M, mx::padded(K) / 2));
+    MX_TRY(check_blob_limit(name, "B (one group)", N, mx::padded(K) / 2));
+    if (!mx::grouped_gemm_fits(M, N, groups))
+        return fail(MX_ERR_UNSUPPORTED, "%s: M=%lld N=%lld in %d groups needs too many output tiles", name,
+                    (long long)M, (long long)N, groups);
+    if (M == 0 || N == 0) return MX_SUCCESS;
+    MX_TRY(check_device());
+    const mx::GroupedGemmArgs a{group_ends, groups, M, N, K, static_cast<const uint8_t *>(A),
+                                static_cast<const uint8_t *>(A_scale), static_cast<const uint8_t *>(B),
+                                static_cast<const uint8_t *>(B_scale), static_cast<const uint16_t *>(bias), out_dtype,
+                                C, ldc, 0};
+    return check_launch(mx::launch_gemm_grouped(a, stream), name);
+}
+
+mx_status mx_gemm_a4w4_grouped_wgrad(int64_t M, int64_t N, int64_t K, const int32_t *group_ends, int groups,
+                                     const void *A, const void *A_scale, const void *B, const void *B_scale,
+                                     mx_layout layout, mx_dtype out_dtype, void *C, int64_t ldc, int64_t group_stride,
+                                     hipStream_t stream) {
+    const char *name = "mx_gemm_a4w4_grouped_wgrad";
+    MX_TRY(check_grouped_gemm(name, M, N, K, group_ends, groups, A, A_scale, B, B_scale, layout, out_dtype, C, ldc, K,
+                              M > 0));
+    // (a stride too large for the product cannot be an allocated tensor)
+    if (groups > 1 && (ldc >= (int64_t(1) << 40) || group_stride < N * ldc))
+        return fail(MX_ERR_INVALID_ARGUMENT, "group_stride=%lld must be >= N * ldc", (long long)group_stride);
+    if (group_stride % 8) return fail(MX_ERR_MISALIGNED, "group_stride=%lld must be a multiple of 8", (long long)group_stride);
+    // a group's part holds at most padded(M) rows
+    MX_TRY(check_blob_limit(name, "A", N, mx::padded(M) / 2));
+    MX_TRY(check_blob_limit(name, "B", K, mx::padded(M) / 2));
+    if (!mx::grouped_wgrad_fits(N, K, groups))
+        return fail(MX_ERR_UNSUPPORTED, "%s: N=%lld K=%lld in %d groups needs too many output tiles", name,
+                    (long long)N, (long long)K, groups);
+    if (N == 0 || K == 0) return MX_SUCCESS;
+    MX_TRY(check_device());
+    const mx::GroupedGemmArgs a{group_ends, groups, M, N, K, static_cast<const uint8_t *>(A),
+                                static_cast<const uint8_t *>(A_scale), static_cast<const uint8_t *>(B),
+                                static_cast<const uint8_t *>(B_scale), nullptr, out_dtype, C, ldc, group_stride};
+    return check_launch(mx::launch_gemm_grouped_wgrad(a, stream), name);
+}
+
+namespace {
+
+mx_status check_adamw_opts(const mx_adamw_opts *o) {
+    if (!o) return fail(MX_ERR_INVALID_ARGUMENT, "opts is NULL");
+    if (!std::isfinite(o->lr) || !std::isfinite(o->weight_decay) || !std::isfinite(o->eps))
+        return fail(MX_ERR_INVALID_ARGUMENT, "lr, weight_decay and eps must be finite");
+    if (!(o->beta1 >= 0 && o->beta1 < 1) || !(o->beta2 >= 0 && o->beta2 < 1))
+        return fail(MX_ERR_INVALID_ARGUMENT, "beta1=%g and beta2=%g must be in [0, 1)", o->beta1, o->beta2);
+    if (o->eps < 0) return fail(MX_ERR_INVALID_ARGUMENT, "eps=%g must be >= 0", o->eps);
+    if (o->step < 1) return fail(MX_ERR_INVALID_ARGUMENT, "step=%lld must be >= 1", (long long)o->step);
+    return MX_SUCCESS;
+}
+
+mx_adamw_step step_of(const mx_adamw_opts &o) {
+    mx_adamw_step s;
+    s.grad_scale = (float)o.grad_scale;
+    s.decay = (float)(1.0 - o.lr * o.weight_decay);
+    s.step_size = (float)(o.lr / (1.0 - std::pow(o.beta1, (double)o.step)));
+    s.root_factor = (float)(1.0 / std::sqrt(1.0 - std::pow(o.beta2, (double)o.step)));
+    s.seed = o.seed;
+    return s;
+}
+
+bool float_dtype(int t) { return t == MX_F32 || t == MX_BF16; }
+
+// Chunks of one launch: a grid of 256-thread workgroups must stay below 2^32 threads.
+constexpr int64_t kMaxChunks = int64_t(1) << 23;
+
+}  // namespace
+
+mx_status mx_adamw_step_values(const mx_adamw_opts *opts, mx_adamw_step *step) {
+    MX_TRY(check_adamw_opts(opts));
+    if (!step) return fail(MX_ERR_INVALID_ARGUMENT, "step is NULL");
+    *step = step_of(*opts);
+    return MX_SUCCESS;
+}
+
+mx_status mx_adamw(const mx_adamw_tensor *tensors, int64_t count, const mx_adamw_opts *opts, hipStream_t stream) {
+    MX_TRY(check_adamw_opts(opts));
+    if (!float_dtype(opts->param_dtype) || !float_dtype(opts->grad_dtype))
+        return fail(MX_ERR_UNSUPPORTED, "param_dtype %d, grad_dtype %d (valid: MX_BF16=0, MX_F32=1)", opts->param_dtype,
+                    opts->grad_dtype);
+    if (opts->state_dtype != MX_STATE_F32 && opts->state_dtype != MX_STATE_MXFP8)
+        return fail(MX_ERR_UNSUPPORTED, "state_dtype %d (valid: MX_STATE_F32=0, MX_STATE_MXFP8=1)", opts->state_dtype);
+    if (opts->use_sr > 1) return fail(MX_ERR_INVALID_ARGUMENT, "use_sr must be 0 or 1");
+    if (reinterpret_cast<uintptr_t>(opts->device_step) & 7u)
+        return fail(MX_ERR_MISALIGNED, "device_step must be 8-byte aligned");
+    if (count < 0 || (count > 0 && !tensors)) return fail(MX_ERR_INVALID_ARGUMENT, "tensors is NULL or count negative");
+    const bool s8 = opts->state_dtype == MX_STATE_MXFP8;
+    for (int64_t i = 0; i < count; ++i) {
+        const mx_adamw_tensor &t = tensors[i];
+        if (t.numel < 0) return fail(MX_ERR_INVALID_ARGUMENT, "tensor %lld: negative numel", (long long)i);
+        if (t.numel > (int64_t(1) << 33))
+            return fail(MX_ERR_UNSUPPORTED, "tensor %lld: numel=%lld is above 2^33", (long long)i, (long long)t.numel);
+        if (t.numel == 0) continue;
+        if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq)
+            return fail(MX_ERR_INVALID_ARGUMENT, "tensor %lld: NULL pointer", (long long)i);
+        if (s8 && (!t.exp_avg_scale || !t.exp_avg_sq_scale))
+            return fail(MX_ERR_INVALID_ARGUMENT, "tensor %lld: MXFP8 states need their scales", (long long)i);
+        if (!aligned16(t.param) || !aligned16(t.grad) || !aligned16(t.exp_avg) || !aligned16(t.exp_avg_sq) ||
+            !aligned16(t.param_copy))
+            return fail(MX_ERR_MISALIGNED, "tensor %lld: pointers must be 16-byte aligned", (long long)i);
+        if (t.param_copy && opts->param_dtype != MX_F32)
+            return fail(MX_ERR_UNSUPPORTED, "tensor %lld: a bf16 copy needs fp32 parameters", (long long)i);
+    }
+    mx::AdamwBatch b{};
+    b.beta1 = (float)opts->beta1;
+    b.one_minus_beta1 = (float)(1.0 - opts->beta1);
+    b.beta2 = (float)opts->beta2;
+    b.one_minus_beta2 = (float)(1.0 - opts->beta2);
+    b.eps = (float)opts->eps;
+    b.step = step_of(*opts);
+    b.dev_step = opts->device_step;
+    int64_t chunks = 0;
+    const auto flush = [&]() -> mx_status {
+        if (b.count == 0) return MX_SUCCESS;
+        const hipError_t e = mx::launch_adamw(b, opts->param_dtype == MX_F32, opts->grad_dtype == MX_F32, s8,
+                                              opts->use_sr != 0, stream);
+        b.count = 0;
+        chunks = 0;
+        return check_launch(e, "mx_adamw");
+    };
+    bool checked = false;
+    for (int64_t i = 0; i < count; ++i) {
+        const mx_adamw_tensor &t = tensors[i];
+        if (t.numel == 0) continue;
+        if (!checked) MX_TRY(check_device());
+        checked = true;
+        const int64_t n = mx::adamw_chunks(t.numel);
+        if (b.count == mx::kAdamwItems || chunks + n > kMaxChunks) MX_TRY(flush());
+        chunks += n;
+        b.t[b.count++] = mx::AdamwItem{t.param, t.grad, t.exp_avg, t.exp_avg_sq,
+                                       static_cast<uint8_t *>(t.exp_avg_scale),
+                                       static_cast<uint8_t *>(t.exp_avg_sq_scale), t.param_copy, t.numel,
+                                       (uint32_t)chunks, t.tensor_id};
+    }
+    return flush();
 }
 
 mx_status mx_layout_convert(int to_tiled, int64_t rows, int64_t length, const void *q_src, const void *s_src,

@@ -35,7 +35,44 @@ struct QuantArgs {
     uint32_t sr_pairs;          // 1: N and both index bases are multiples of 16
     uint8_t *q_row, *s_row, *q_col, *s_col;
     int64_t row_tile0;          // first 128-row tile of this launch (set by the launchers)
+    // grouped quantization: cumulative row ends of the groups and, optionally,
+    // the row of x (x_rows of them) that each grouped row is
+    const int32_t *ends, *row_index;
+    int32_t groups;
+    int64_t x_rows;
 };
+
+struct GroupedGemmArgs {
+    const int32_t *ends;        // cumulative row ends of the groups, device memory
+    int groups;
+    int64_t M, N, K;            // M: rows of all groups
+    const uint8_t *A, *As, *B, *Bs;
+    const uint16_t *bias;       // groups x N, or NULL
+    mx_dtype out_dtype;
+    void *C;
+    int64_t ldc, group_stride;
+};
+
+// Descriptors of one AdamW launch, passed as kernel arguments.
+struct AdamwItem {
+    void *param;
+    const void *grad;
+    void *m, *v;
+    uint8_t *ms, *vs;           // block scales of 8-bit states
+    void *copy;                 // bf16 copy of the parameters, or NULL
+    int64_t numel;
+    uint32_t chunk_end;         // workgroups of this and the items before it
+    uint32_t tensor_id;
+};
+constexpr int kAdamwItems = 48;
+struct AdamwBatch {
+    AdamwItem t[kAdamwItems];
+    int count;
+    float beta1, one_minus_beta1, beta2, one_minus_beta2, eps;
+    mx_adamw_step step;
+    const mx_adamw_step *dev_step;
+};
+static_assert(sizeof(AdamwBatch) <= 4000, "kernel arguments");
 
 // Grid dimension y of one launch holds at most 65536 workgroups on gfx950
 // (hipDeviceAttributeMaxGridDimY); the quantize launchers cover taller inputs
@@ -60,6 +97,13 @@ hipError_t launch_quantize_fp8(const uint16_t *x, int64_t M, int64_t N, int64_t 
                                uint8_t *q_row, uint8_t *q_col, float *info, hipStream_t stream);
 hipError_t launch_layout_convert(bool to_tiled, int64_t rows, int64_t length, const uint8_t *q_src,
                                  const uint8_t *s_src, uint8_t *q_dst, uint8_t *s_dst, hipStream_t stream);
+hipError_t launch_quantize_grouped(const QuantArgs &a, bool dual, hipStream_t stream);
+bool grouped_gemm_fits(int64_t M, int64_t N, int groups);
+bool grouped_wgrad_fits(int64_t N, int64_t K, int groups);
+hipError_t launch_gemm_grouped(const GroupedGemmArgs &a, hipStream_t stream);
+hipError_t launch_gemm_grouped_wgrad(const GroupedGemmArgs &a, hipStream_t stream);
+int64_t adamw_chunks(int64_t numel);   // workgroups that numel elements take
+hipError_t launch_adamw(const AdamwBatch &b, bool p32, bool g32, bool s8, bool sr, hipStream_t stream);
 hipError_t launch_dequantize(const uint8_t *q, const uint8_t *s, int64_t rows, int64_t length,
                              mx_layout layout, float *out, int64_t ldo, hipStream_t stream);
 hipError_t launch_measure_mfma(int fmt_a, int fmt_b, const void *ops, int workgroups, int64_t iters, float *out,

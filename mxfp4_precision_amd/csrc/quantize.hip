@@ -49,7 +49,7 @@
 // 130, 200 and 254: no difference), SR from exact fraction bits of
 // |y| 2^(127-c).
 
-#include "mx_internal.h"
+#include "grouped.h"
 
 namespace mx {
 namespace {
@@ -505,7 +505,11 @@ constexpr int kMinWaves = (DUAL && (ROW_SR || COL_SR) && !RHT) ? (ELEM == 6 ? (R
 // 64 bytes (FP4) or 96 bytes (FP6), padded by 16 bytes against bank conflicts.
 // MUL: the quantized tensor is bf16(x * g) elementwise (the prologue of
 // mx_quantize_dual_mul), formed in the staging read.
-template <int ELEM, int LAYOUT, bool DUAL, bool ROW_SR, bool COL_SR, bool RHT, bool MUL = false>
+// GROUPED: the rows come in groups (grouped.h), each of which becomes the
+// blobs that its rows alone would give; a tile of 128 rows lies in one group.
+// With a row index, row r of the grouped order is row index[r] of x, and an
+// index outside [0, x_rows) gives a row of zeros.
+template <int ELEM, int LAYOUT, bool DUAL, bool ROW_SR, bool COL_SR, bool RHT, bool MUL = false, bool GROUPED = false>
 __global__ __launch_bounds__(256) __attribute__((
     amdgpu_waves_per_eu(kMinWaves<ELEM, DUAL, ROW_SR, COL_SR, RHT>, 8))) void quantize_kernel(QuantArgs a) {
     static_assert(ELEM == 4 || (ELEM == 6 && !RHT), "element size");
@@ -515,7 +519,28 @@ __global__ __launch_bounds__(256) __attribute__((
     const int wave = threadIdx.x >> 6;
     const int c = lane & 15;
     const int q = lane >> 4;
-    const int64_t row0 = ((int64_t)blockIdx.y + a.row_tile0) * kTileRows + wave * kWaveRows;
+    int64_t row0 = ((int64_t)blockIdx.y + a.row_tile0) * kTileRows + wave * kWaveRows;
+    int64_t group_start = 0;   // rows of x before the group
+    if constexpr (GROUPED) {
+        GroupPos p;
+        const int tile = (int)(blockIdx.y + a.row_tile0);
+        if (!find_tile<kTileRows>(a.ends, a.groups, (int)a.M, [&](int) { return tile; }, p)) return;
+        if (p.group >= a.groups) return;   // rows in no group
+        // from here on, the group's rows as a tensor of their own
+        const int64_t n16 = cdiv(a.N, 16) * 16;
+        a.M = p.rows;
+        a.M_pad = padded(p.rows);
+        a.q_row += (int64_t)p.r16 * 16 * (a.N_pad / 2);
+        a.s_row += (int64_t)p.r16 * 16 * (cdiv(a.N_pad, 512) * 16);
+        if (DUAL) {
+            a.q_col += (int64_t)p.k128 * n16 * 64;
+            a.s_col += (int64_t)p.k512 * n16 * 16;
+        }
+        a.row.index_base += (uint64_t)p.start * (uint64_t)a.N;
+        a.col.index_base += (uint64_t)p.start * (uint64_t)a.N;
+        group_start = p.start;
+        row0 = (int64_t)p.tile * kTileRows + wave * kWaveRows;
+    }
     const int64_t col0 = (int64_t)blockIdx.x * kTileCols;
     const int64_t M = a.M, N = a.N;
     // real rows among the lane's 8 (8q..8q+7) and real columns among its 8 (8c..8c+7)
@@ -532,15 +557,25 @@ __global__ __launch_bounds__(256) __attribute__((
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
         const int64_t i = row0 + 8 * q + t;
-        const uint16_t *p = a.x + i * a.ldx + j0;
-        if (i < M && j0 + 8 <= N) {
+        int64_t src = i;
+        bool real = i < M;
+        if constexpr (GROUPED) {
+            src += group_start;
+            if (a.row_index) {
+                const int32_t at = real ? a.row_index[src] : -1;
+                real = at >= 0 && at < a.x_rows;
+                src = at;
+            }
+        }
+        const uint16_t *p = a.x + src * a.ldx + j0;
+        if (real && j0 + 8 <= N) {
             const v4u_t v = __builtin_nontemporal_load(reinterpret_cast<const v4u_t *>(p));
             d[t][0] = v.x; d[t][1] = v.y; d[t][2] = v.z; d[t][3] = v.w;
         } else {
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                uint32_t lo = (i < M && j0 + 2 * w < N) ? p[2 * w] : 0u;
-                uint32_t hi = (i < M && j0 + 2 * w + 1 < N) ? p[2 * w + 1] : 0u;
+                uint32_t lo = (real && j0 + 2 * w < N) ? p[2 * w] : 0u;
+                uint32_t hi = (real && j0 + 2 * w + 1 < N) ? p[2 * w + 1] : 0u;
                 d[t][w] = lo | (hi << 16);
             }
         }
@@ -1164,6 +1199,40 @@ hipError_t launch_quantize_fp6(const QuantArgs &a, bool dual, mx_layout layout, 
         return dual ? launch_sr<6, MX_LAYOUT_TILED, true, false>(b, grid, stream)
                     : launch_sr<6, MX_LAYOUT_TILED, false, false>(b, grid, stream);
     });
+}
+
+template <bool DUAL, bool RHT>
+hipError_t launch_grouped(const QuantArgs &a, dim3 grid, hipStream_t stream) {
+    constexpr int T = MX_LAYOUT_TILED;
+    auto kernel = a.row.use_sr ? quantize_kernel<4, T, DUAL, true, false, RHT, false, true>
+                               : quantize_kernel<4, T, DUAL, false, false, RHT, false, true>;
+    if constexpr (DUAL) {
+        if (a.col.use_sr)
+            kernel = a.row.use_sr ? quantize_kernel<4, T, true, true, true, RHT, false, true>
+                                  : quantize_kernel<4, T, true, false, true, RHT, false, true>;
+    }
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+// Grid rows: the most 128-row tiles that M rows in a.groups groups can need;
+// workgroups past those that there are return at once.
+hipError_t launch_quantize_grouped(const QuantArgs &a, bool dual, hipStream_t stream) {
+    const int64_t full = a.groups < a.M ? a.groups : a.M;
+    QuantArgs b = a;
+    const int64_t row_tiles = (a.M + (kTileRows - 1) * full) / kTileRows;
+    for (int64_t t0 = 0; t0 < row_tiles; t0 += kMaxRowTiles) {
+        b.row_tile0 = t0;
+        const dim3 grid((unsigned)cdiv(a.N, kTileCols),
+                        (unsigned)(row_tiles - t0 < kMaxRowTiles ? row_tiles - t0 : kMaxRowTiles));
+        const bool rht = a.row.rht || (dual && a.col.rht);
+        const hipError_t e = dual ? (rht ? launch_grouped<true, true>(b, grid, stream)
+                                         : launch_grouped<true, false>(b, grid, stream))
+                                  : (rht ? launch_grouped<false, true>(b, grid, stream)
+                                         : launch_grouped<false, false>(b, grid, stream));
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace mx
