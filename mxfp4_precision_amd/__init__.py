@@ -173,17 +173,17 @@ def _dptr(p) -> Optional[int]:
     here: a kernel that dereferences a host address faults the device."""
     if p is None or isinstance(p, int):
         return p
-    if hasattr(p, "data_ptr"):
-        if not getattr(p, "is_cuda", False):
-            raise TypeError("a device pointer is required, got a tensor on %s" % p.device)
+    if getattr(p, "is_cuda", False):
         return p.data_ptr()
+    if hasattr(p, "data_ptr"):
+        raise TypeError("a device pointer is required, got a tensor on %s" % p.device)
     raise TypeError("a device pointer is required, got %r (host arrays are not accepted)" % type(p))
 
 
 def _i32ptr(p, count: int) -> Optional[int]:
     """A device pointer to `count` int32 values.  A tensor of another type, with gaps or with fewer values is
     refused: the kernels read that many consecutive 32-bit words."""
-    if hasattr(p, "data_ptr"):
+    if p is not None and not isinstance(p, int) and hasattr(p, "data_ptr"):
         if str(p.dtype) != "torch.int32" or not p.is_contiguous() or p.numel() < count:
             raise TypeError("a contiguous int32 tensor of at least %d values is required, got %s of %s"
                             % (count, p.dtype, tuple(p.shape)))
@@ -204,10 +204,23 @@ def _hptr(p) -> Optional[int]:
     raise TypeError("expected a host array, tensor or int, got %r" % type(p))
 
 
+def _current_stream() -> int:
+    """The handle of torch's current stream.  torch.cuda.current_stream() builds a Stream object for it, which took
+    2.7 us of a 7.7 us call; the handle alone takes 0.2 us."""
+    global _current_stream
+    import torch
+    device, raw = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    torch.cuda.current_stream()     # initializes torch's CUDA state, which the two functions expect
+    if device and raw:
+        _current_stream = lambda: raw(device())  # noqa: E731
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _current_stream()
+
+
 def _stream(s) -> Optional[int]:
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
