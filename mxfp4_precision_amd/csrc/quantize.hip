@@ -1201,6 +1201,113 @@ hipError_t launch_quantize_fp6(const QuantArgs &a, bool dual, mx_layout layout, 
     });
 }
 
+// Grouped rows, row-wise blob only, nearest even, blocks of 32: what serving
+// needs, in a kernel short enough that its latency is three dependent loads
+// (ends, index, row).  A wave takes 16 rows x 512 columns: 4 data atoms and
+// one scale atom.  Lane L reads 8 elements of rows 4 t + L / 16 (256
+// consecutive bytes of a row per 16 lanes), a block is a quad of lanes, and a
+// 4 x 4 transpose inside the quad gives lane L the whole block L % 16 / 4 of
+// row 4 (L % 4) + L / 16: one 16-byte store per atom, one dword of scales.
+// The 16-row units of all groups, counted through, are the blob's row groups.
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int lane) {
+    const auto exchange = [](uint32_t &a, uint32_t &b, bool odd, auto dpp) {
+        const uint32_t got = dpp(odd ? a : b);
+        if (odd) a = got;
+        else b = got;
+    };
+    const auto by1 = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false); };
+    const auto by2 = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false); };
+    exchange(w[0], w[1], lane & 1, by1);
+    exchange(w[2], w[3], lane & 1, by1);
+    exchange(w[0], w[2], lane & 2, by2);
+    exchange(w[1], w[3], lane & 2, by2);
+}
+
+__global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a, uint32_t chunks) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int unit = (int)(id / chunks), chunk = (int)(id % chunks);
+    int start = 0, rows = 0, before = 0;   // the unit's group, and the units before it
+    {
+        GroupCarry c;
+        bool found = false;
+        for (int base = 0; base < a.groups; base += 64) {
+            const GroupLane g = group_block<16, false>(a.ends, a.groups, (int)a.M, base, lane, c);
+            const uint64_t past = __builtin_amdgcn_ballot_w64(unit < g.tiles);
+            if (past) {
+                const int l = __builtin_ctzll(past);
+                start = __builtin_amdgcn_readlane(g.start, l);
+                rows = __builtin_amdgcn_readlane(g.rows, l);
+                before = __builtin_amdgcn_readlane(g.tiles, l) - units(rows, 16);
+                found = true;
+                break;
+            }
+        }
+        if (!found) return;
+    }
+    const int row0 = (unit - before) * 16;
+    const int64_t col0 = (int64_t)chunk * 512 + 8 * (lane & 15);
+    v4u_t d[4][4];   // [atom][t]
+    const uint16_t *src[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int r = row0 + 4 * t + (lane >> 4);
+        int64_t at = (int64_t)start + r;
+        bool real = r < rows;
+        if (a.row_index) {
+            at = real ? a.row_index[at] : -1;
+            real = at >= 0 && at < a.x_rows;
+        }
+        src[t] = real ? a.x + at * a.ldx : nullptr;
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int64_t j = col0 + 128 * m;
+            d[m][t] = v4u_t{0u, 0u, 0u, 0u};
+            if (src[t]) {
+                if (j + 8 <= a.N) {
+                    d[m][t] = *reinterpret_cast<const v4u_t *>(src[t] + j);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 7; ++e)
+                        if (j + e < a.N) d[m][t][e >> 1] |= (uint32_t)src[t][j + e] << (16 * (e & 1));
+                }
+            }
+        }
+    const int64_t ksteps = a.N_pad / 128, kgroups = cdiv(a.N_pad, 512);
+    const int slot = 4 * (lane & 3) + (lane >> 4) + 16 * ((lane & 15) >> 2);   // row + 16 * block of the stores
+    uint32_t scales[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        uint32_t w[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const v4u_t v = d[m][t];
+            uint32_t amax = pk_umax(pk_umax(v[0] & 0x7FFF7FFFu, v[1] & 0x7FFF7FFFu),
+                                    pk_umax(v[2] & 0x7FFF7FFFu, v[3] & 0x7FFF7FFFu));
+            amax = lane_max<2, true>(lane_max<1, true>(amax));
+            bool nonfinite;
+            const uint32_t c = scale_code_nf(umax(amax & 0xFFFFu, amax >> 16), nonfinite);
+            w[t] = pack8_rne(v[0], v[1], v[2], v[3], c, nonfinite);
+            scales[t] |= c << (8 * m);
+        }
+        quad_transpose(w, lane);
+        if (4 * (int64_t)chunk + m < ksteps)
+            *reinterpret_cast<v4u_t *>(a.q_row + ((int64_t)unit * ksteps + 4 * chunk + m) * 1024 + slot * 16) =
+                v4u_t{w[0], w[1], w[2], w[3]};
+    }
+    const uint32_t s01 = lane & 1 ? scales[1] : scales[0], s23 = lane & 1 ? scales[3] : scales[2];
+    *reinterpret_cast<uint32_t *>(a.s_row + ((int64_t)unit * kgroups + chunk) * 256 + slot * 4) = lane & 2 ? s23 : s01;
+}
+
+// Workgroups of a quantize_rows_kernel launch.
+int64_t quantize_rows_blocks(const QuantArgs &a) {
+    const int64_t full = a.groups < a.M ? a.groups : a.M;
+    return cdiv((a.M + 15 * full) / 16 * cdiv(a.N_pad, 512), 4);
+}
+
 template <bool DUAL, bool RHT>
 hipError_t launch_grouped(const QuantArgs &a, dim3 grid, hipStream_t stream) {
     constexpr int T = MX_LAYOUT_TILED;
@@ -1218,6 +1325,12 @@ hipError_t launch_grouped(const QuantArgs &a, dim3 grid, hipStream_t stream) {
 // Grid rows: the most 128-row tiles that M rows in a.groups groups can need;
 // workgroups past those that there are return at once.
 hipError_t launch_quantize_grouped(const QuantArgs &a, bool dual, hipStream_t stream) {
+    // (a grid holds fewer than 2^32 threads)
+    if (!dual && !a.row.use_sr && !a.row.use_2d && !a.row.rht && quantize_rows_blocks(a) < int64_t(1) << 24) {
+        hipLaunchKernelGGL(quantize_rows_kernel, dim3((unsigned)quantize_rows_blocks(a)), dim3(256), 0, stream, a,
+                           (uint32_t)cdiv(a.N_pad, 512));
+        return hipGetLastError();
+    }
     const int64_t full = a.groups < a.M ? a.groups : a.M;
     QuantArgs b = a;
     const int64_t row_tiles = (a.M + (kTileRows - 1) * full) / kTileRows;
