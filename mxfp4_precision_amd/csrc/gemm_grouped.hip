@@ -93,6 +93,160 @@ __global__ __launch_bounds__(C::kThreads) void gemm_grouped_kernel(const int32_t
                             wave, wave, lane);
 }
 
+// ------------------------------------------------------------ few rows
+// Groups of few rows (decoding): what counts is reading the weights once and
+// the latency of one pass, so B does not go through LDS.  An atom (16 rows x
+// 128 k) is exactly the operand of V_MFMA_SCALE_F32_16X16X128_F8F6F4: lane L
+// holds row L % 16, block L / 16, 16 bytes at 16 L, and loads them straight
+// into registers.  A workgroup's tile is 64 rows (or the group's remainder,
+// MA atoms) x 32 columns; its four waves take k-step 4 h + wave of every
+// k-group h, so each reads one byte of the scale dwords that all four load,
+// and their sums are added in wave order through LDS.  kDepth k-groups are
+// in flight per wave.
+constexpr int kFewM = 64, kFewNB = 2, kFewN = 16 * kFewNB;
+
+template <int MA, int DEPTH>
+__device__ __forceinline__ void few_rows_sum(__amdgpu_buffer_rsrc_t rA, __amdgpu_buffer_rsrc_t rAs,
+                                             __amdgpu_buffer_rsrc_t rB, __amdgpu_buffer_rsrc_t rBs, int gA0, int nGA,
+                                             int gB0, int nGB, int ksteps, int kgroups, int wave, int lane,
+                                             v4f (&acc)[kFewM / 16][kFewNB]) {
+    // atom rows past an operand are clamped to its last one: those results are not stored
+    int a_row[MA], b_row[kFewNB];
+#pragma unroll
+    for (int i = 0; i < MA; ++i) a_row[i] = min(gA0 + i, nGA - 1);
+#pragma unroll
+    for (int j = 0; j < kFewNB; ++j) b_row[j] = min(gB0 + j, nGB - 1);
+    const uint32_t lane16 = (uint32_t)lane * 16, lane4 = (uint32_t)lane * 4;
+    for (int h0 = 0; h0 < kgroups; h0 += DEPTH) {
+        v4u_t a[DEPTH][MA], b[DEPTH][kFewNB];
+        uint32_t as[DEPTH][MA], bs[DEPTH][kFewNB];
+#pragma unroll
+        for (int u = 0; u < DEPTH; ++u) {
+            const int h = h0 + u, ks = 4 * h + wave;
+            // Past K both read as zeros: the lane offset is out of range on its
+            // own, the scalar one is then 0 (the range check subtracts it from
+            // the range).
+            const bool in = ks < ksteps, sin = h < kgroups;
+            const uint32_t off = in ? lane16 : kOutOfRange, soff = sin ? lane4 : kOutOfRange;
+#pragma unroll
+            for (int j = 0; j < kFewNB; ++j) {
+                b[u][j] = __builtin_amdgcn_raw_buffer_load_b128(rB, off, in ? (b_row[j] * ksteps + ks) * 1024 : 0, 0);
+                bs[u][j] = __builtin_amdgcn_raw_buffer_load_b32(rBs, soff, sin ? (b_row[j] * kgroups + h) * 256 : 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < MA; ++i) {
+                a[u][i] = __builtin_amdgcn_raw_buffer_load_b128(rA, off, in ? (a_row[i] * ksteps + ks) * 1024 : 0, 0);
+                as[u][i] = __builtin_amdgcn_raw_buffer_load_b32(rAs, soff, sin ? (a_row[i] * kgroups + h) * 256 : 0, 0);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < DEPTH; ++u)
+#pragma unroll
+            for (int i = 0; i < MA; ++i)
+#pragma unroll
+                for (int j = 0; j < kFewNB; ++j) {
+                    const v8i bop = {(int)b[u][j][0], (int)b[u][j][1], (int)b[u][j][2], (int)b[u][j][3], 0, 0, 0, 0};
+                    const v8i aop = {(int)a[u][i][0], (int)a[u][i][1], (int)a[u][i][2], (int)a[u][i][3], 0, 0, 0, 0};
+                    const int sb = (int)(bs[u][j] >> (8 * wave)), sa = (int)(as[u][i] >> (8 * wave));
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bop, aop, acc[i][j], Fp4Fmt::kFb,
+                                                                                 Fp4Fmt::kFa, 0, sb, 0, sa);
+                }
+    }
+}
+
+template <bool OUT_BF16, bool BIAS>
+__global__ __launch_bounds__(256) void gemm_grouped_few_kernel(const int32_t *__restrict__ ends, int groups, int M,
+                                                               int N, int K_pad, int tiles_n,
+                                                               const uint8_t *__restrict__ A,
+                                                               const uint8_t *__restrict__ As,
+                                                               const uint8_t *__restrict__ B,
+                                                               const uint8_t *__restrict__ Bs,
+                                                               const uint16_t *__restrict__ bias,
+                                                               void *__restrict__ Cout, int64_t ldc) {
+    constexpr int kTiles = kFewM / 16 * kFewNB;
+    __shared__ v4f s_sum[4][kTiles][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int tn = 0;
+    GroupPos p;
+    const bool found = find_tile<kFewM>(ends, groups, M, [&](int total_m) {
+        const int id = xcd_position(blockIdx.x, total_m * tiles_n);
+        if (id < 0) return -1;
+        tn = id % tiles_n;
+        return id / tiles_n;
+    }, p);
+    if (!found) return;
+    const bool live = p.group < groups;
+    const int row0 = p.tile * kFewM;
+    const int ma = min((p.rows - row0 + 15) / 16, kFewM / 16);
+    v4f acc[kFewM / 16][kFewNB];
+#pragma unroll
+    for (int i = 0; i < kFewM / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < kFewNB; ++j) acc[i][j] = v4f{};
+    const int ksteps = K_pad / 128, kgroups = (K_pad + 511) / 512;
+    if (live && ksteps > 0) {
+        const int nGA = (p.rows + 15) / 16, nGB = (N + 15) / 16;
+        const int64_t gB = (int64_t)p.group * nGB;
+        const auto rA = make_rsrc(A + (int64_t)p.r16 * ksteps * 1024, (int64_t)nGA * ksteps * 1024);
+        const auto rAs = make_rsrc(As + (int64_t)p.r16 * kgroups * 256, (int64_t)nGA * kgroups * 256);
+        const auto rB = make_rsrc(B + gB * ksteps * 1024, (int64_t)nGB * ksteps * 1024);
+        const auto rBs = make_rsrc(Bs + gB * kgroups * 256, (int64_t)nGB * kgroups * 256);
+        const int gA0 = row0 / 16, gB0 = tn * kFewNB;
+        if (ma == 1) few_rows_sum<1, 8>(rA, rAs, rB, rBs, gA0, nGA, gB0, nGB, ksteps, kgroups, wave, lane, acc);
+        else if (ma == 2) few_rows_sum<2, 4>(rA, rAs, rB, rBs, gA0, nGA, gB0, nGB, ksteps, kgroups, wave, lane, acc);
+        else few_rows_sum<4, 4>(rA, rAs, rB, rBs, gA0, nGA, gB0, nGB, ksteps, kgroups, wave, lane, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < kFewM / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < kFewNB; ++j)
+            if (i < ma) s_sum[wave][i * kFewNB + j][lane] = acc[i][j];
+    __syncthreads();
+    // lane L of tile (i, j): row 16 i + L % 16, columns 16 j + 4 (L / 16) + 0..3
+    for (int t = wave; t < ma * kFewNB; t += 4) {
+        v4f v = s_sum[0][t][lane];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) {
+            const v4f q = s_sum[w][t][lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += q[e];
+        }
+        const int row = row0 + 16 * (t / kFewNB) + (lane & 15);
+        const int col = tn * kFewN + 16 * (t % kFewNB) + 4 * (lane >> 4);
+        if (row >= p.rows || col >= N) continue;
+        if constexpr (BIAS) {
+            if (live) {
+                const uint16_t *b = bias + (int64_t)p.group * N + col;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (col + e < N) v[e] += __uint_as_float((uint32_t)b[e] << 16);
+            }
+        }
+        const int64_t at = ((int64_t)p.start + row) * ldc + col;
+        if constexpr (OUT_BF16) {
+            uint16_t *dst = static_cast<uint16_t *>(Cout) + at;
+            const v2u_t w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            if (col + 3 < N) {
+                *reinterpret_cast<v2u_t *>(dst) = w;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    if (col + e < N) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+            }
+        } else {
+            float *dst = static_cast<float *>(Cout) + at;
+            if (col + 3 < N) {
+                *reinterpret_cast<v4f *>(dst) = v;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    if (col + e < N) dst[e] = v[e];
+            }
+        }
+    }
+}
+
 // wgrad: workgroup -> (group, tile of its M x N product); K = the group's rows.
 template <class C, bool OUT_BF16>
 __global__ __launch_bounds__(C::kThreads) void gemm_grouped_wgrad_kernel(const int32_t *__restrict__ ends, int groups,
@@ -159,6 +313,17 @@ hipError_t launch_shape(const GroupedGemmArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+hipError_t launch_few(const GroupedGemmArgs &a, hipStream_t stream) {
+    const int tiles_n = (int)cdiv(a.N, kFewN);
+    const int64_t blocks = cdiv(max_tiles(a.M, a.groups, kFewM) * tiles_n, kXcds) * kXcds;
+    const bool bf = a.out_dtype == MX_BF16;
+    auto kernel = bf ? (a.bias ? gemm_grouped_few_kernel<true, true> : gemm_grouped_few_kernel<true, false>)
+                     : (a.bias ? gemm_grouped_few_kernel<false, true> : gemm_grouped_few_kernel<false, false>);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a.ends, a.groups, (int)a.M, (int)a.N,
+                       (int)padded(a.K), tiles_n, a.A, a.As, a.B, a.Bs, a.bias, a.C, a.ldc);
+    return hipGetLastError();
+}
+
 template <class S>
 hipError_t launch_wgrad_shape(const GroupedGemmArgs &a, hipStream_t stream) {
     using C = Cfg<Fp4Fmt, S>;
@@ -177,7 +342,7 @@ hipError_t launch_wgrad_shape(const GroupedGemmArgs &a, hipStream_t stream) {
 constexpr int64_t kMaxBlocks = int64_t(1) << 22;
 
 bool grouped_gemm_fits(int64_t M, int64_t N, int groups) {
-    return max_tiles(M, groups, 128) * cdiv(N, 128) < kMaxBlocks;
+    return max_tiles(M, groups, 64) * cdiv(N, 32) < kMaxBlocks;
 }
 
 bool grouped_wgrad_fits(int64_t N, int64_t K, int groups) {
@@ -185,6 +350,7 @@ bool grouped_wgrad_fits(int64_t N, int64_t K, int groups) {
 }
 
 hipError_t launch_gemm_grouped(const GroupedGemmArgs &a, hipStream_t stream) {
+    if (a.M <= 32 * (a.groups < a.M ? a.groups : a.M)) return launch_few(a, stream);
     return a.M >= 128 * (int64_t)a.groups ? launch_shape<MainShape>(a, stream) : launch_shape<TailShape>(a, stream);
 }
 
