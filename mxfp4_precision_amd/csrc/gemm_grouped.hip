@@ -293,6 +293,250 @@ __global__ __launch_bounds__(C::kThreads) void gemm_grouped_wgrad_kernel(const i
                             wave, lane);
 }
 
+// ------------------------------------------------------------ persistent form
+// One workgroup per CU runs its 256x256 tiles as one stream of k-steps, as
+// the persistent form of gemm.hip does (the next tile's first steps are
+// fetched during the current tile's last ones, the stores drain while the
+// next tile computes).  Here the next tile may lie in another group: every
+// offset counts from the whole blob (both blobs below 2 GiB), so crossing a
+// group changes scalars only, and with WGRAD a tile's number of k-steps
+// changes too.  What a tile needs of its group is looked up in a table that
+// the workgroup builds in LDS at its start: at 16-32 k-steps per tile the
+// ends' load and scan in front of each tile cost about a tenth of it.  A tile
+// without k-steps (rows in no group; a group without rows) runs one k-group
+// of zeros.
+//
+// An XCD's workgroups walk a contiguous range of the tile order round-robin,
+// so that they share A rows and B columns in its L2.  The ranges hold equally
+// many tiles, or, with WGRAD, equally much work: a tile costs its k-steps and
+// about kTileCost more for its stores.
+constexpr int kStreamGroups = 512;   // groups that the table holds
+constexpr int kTileCost = 8;
+
+struct StreamTile {
+    int ksteps;      // 0: zeros
+    int tn, rows;    // column tile; rows of C that the tile has
+    int64_t base;    // element of C where the tile's first row starts
+    int bias;        // index of its group's bias, or -1
+};
+
+// v, as a value that the compiler does not compute ahead of a loop and hold:
+// the k-loop leaves no registers for that.
+__device__ __forceinline__ int hidden(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+template <class C, bool WGRAD, bool BIAS>
+__global__ __launch_bounds__(C::kThreads) void gemm_grouped_stream_kernel(
+    const int32_t *__restrict__ ends, int groups, int grows, int M, int N, int K_pad, int tiles_m, int tiles_n,
+    const uint8_t *__restrict__ A, const uint8_t *__restrict__ As, const uint8_t *__restrict__ B,
+    const uint8_t *__restrict__ Bs, const uint16_t *__restrict__ bias, uint16_t *__restrict__ Cout, int ldc,
+    int64_t group_stride) {
+    // groups: {tiles, or work, of the groups so far; first row; rows; blob units before it}
+    __shared__ int4 s_group[kStreamGroups + 1];
+    __shared__ int s_k512[WGRAD ? kStreamGroups : 1];
+    constexpr int kBiasLoads = BIAS ? C::kMB * 4 : 0;
+    constexpr int kFreshOps = epi_stores<C>() + kBiasLoads;
+    constexpr int kBlob = 0x7FFFFFFF;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wn = wave / C::kWavesM;
+
+    if (wave == 0) {
+        GroupCarry c;
+        int work = 0;
+        for (int base = 0; base < groups; base += 64) {
+            const GroupLane g = group_block<C::kBM, true>(ends, groups, grows, base, lane, c);
+            int sum = g.tiles, before = g.r16 - units(g.rows, 16);
+            if constexpr (WGRAD) {
+                const int kg = units(g.rows, 512);
+                sum = work + wave_scan<false>(base + lane < groups ? 4 * max(kg, 1) + kTileCost : 0);
+                work = __builtin_amdgcn_readlane(sum, 63);
+                before = g.k128 - units(g.rows, 128);
+                if (base + lane < groups) s_k512[base + lane] = g.k512 - kg;
+            }
+            if (base + lane < groups) s_group[base + lane] = int4{sum, g.start, g.rows, before};
+        }
+        const int rest = grows - c.end;
+        if (!WGRAD && lane == 0) s_group[groups] = int4{c.tiles + units(rest, C::kBM), c.end, rest, 0};
+    }
+    __syncthreads();
+
+    // the group whose running sum passes v, and its entry
+    const auto find = [&](int v, int last, int &e, int4 &g) {
+        int lane = hidden(threadIdx.x & 63);
+        for (int base = 0;; base += 64) {
+            const int4 mine = s_group[min(base + lane, last)];
+            const uint64_t past = __builtin_amdgcn_ballot_w64(v < mine.x || base + lane >= last);
+            if (past) {
+                const int l = __builtin_ctzll(past);
+                e = base + l;
+                g = int4{__builtin_amdgcn_readlane(mine.x, l), __builtin_amdgcn_readlane(mine.y, l),
+                         __builtin_amdgcn_readlane(mine.z, l), __builtin_amdgcn_readlane(mine.w, l)};
+                return;
+            }
+        }
+    };
+    int total, at, stop;   // tiles; this workgroup's next one and its XCD's end
+    const int xcd = blockIdx.x % kXcds, step = gridDim.x / kXcds;
+    if constexpr (WGRAD) {
+        tiles_m = (M + C::kBM - 1) / C::kBM;
+        const int per = tiles_m * tiles_n;
+        total = groups * per;
+        const int64_t work = __builtin_amdgcn_readfirstlane(s_group[groups - 1].x);
+        const auto first_of = [&](int x) {
+            if (x == 0) return 0;
+            if (x == kXcds) return total;
+            const int v = (int)(work * x / kXcds);
+            int e;
+            int4 g;
+            find(v, groups - 1, e, g);
+            const int cost = 4 * max(units(g.z, 512), 1) + kTileCost;
+            return e * per + (int)((int64_t)(v - (g.x - cost)) * per / cost);
+        };
+        at = first_of(xcd);
+        stop = first_of(xcd + 1);
+    } else {
+        tiles_m = __builtin_amdgcn_readfirstlane(s_group[groups].x);
+        total = tiles_m * tiles_n;
+        at = (int)((int64_t)total * xcd / kXcds);
+        stop = (int)((int64_t)total * (xcd + 1) / kXcds);
+    }
+    at = __builtin_amdgcn_readfirstlane(at + (int)(blockIdx.x / kXcds));
+    stop = __builtin_amdgcn_readfirstlane(stop);
+    if (at >= stop) return;
+
+    Ctx<C, true> c;
+    c.wave = wave;
+    c.lane16 = lane * 16;
+    c.lane4 = lane * 4;
+    c.rA = make_rsrc(A, kBlob);
+    c.rB = make_rsrc(B, kBlob);
+    c.rAs = make_rsrc(As, kBlob);
+    c.rBs = make_rsrc(Bs, kBlob);
+    const int nGB = (N + 15) / 16;
+    // tile `id`: its values, and the blob offsets of this wave's DMA units
+    const auto resolve = [&](int id, StreamTile &t, int (&lo)[C::kLoLoads], int (&sc)[C::kScaleLoads]) {
+        int tm, nGA, lo_a, lo_b, sc_a, sc_b, kgroups, e;   // blob offsets of the group
+        int4 g;
+        if constexpr (WGRAD) {
+            const int per = tiles_m * tiles_n;
+            e = id / per;
+            const int4 v = s_group[e];
+            g = int4{0, 0, __builtin_amdgcn_readfirstlane(v.z), __builtin_amdgcn_readfirstlane(v.w)};
+            const int k512 = __builtin_amdgcn_readfirstlane(s_k512[e]);
+            tile_at(id - e * per, tiles_m, tiles_n, tiles_m <= 16 ? 4 : 8, tm, t.tn);
+            t.ksteps = units(g.z, 128);
+            kgroups = units(g.z, 512);
+            nGA = (M + 15) / 16;
+            lo_a = g.w * nGA * 1024;
+            lo_b = g.w * nGB * 1024;
+            sc_a = k512 * nGA * 256;
+            sc_b = k512 * nGB * 256;
+            t.rows = M - tm * C::kBM;
+            t.base = e * group_stride + (int64_t)tm * C::kBM * ldc;
+        } else {
+            tile_at(id, tiles_m, tiles_n, tiles_m <= 16 ? 4 : 8, tm, t.tn);
+            find(tm, groups, e, g);
+            tm -= g.x - units(g.z, C::kBM);
+            t.ksteps = e < groups ? K_pad / 128 : 0;
+            kgroups = units(K_pad, 512);
+            nGA = units(g.z, 16);
+            lo_a = g.w * t.ksteps * 1024;
+            sc_a = g.w * kgroups * 256;
+            lo_b = e * nGB * t.ksteps * 1024;
+            sc_b = e * nGB * kgroups * 256;
+            t.rows = g.z - tm * C::kBM;
+            t.base = (int64_t)(g.y + tm * C::kBM) * ldc;
+        }
+        t.bias = e < groups ? e : -1;
+        // (all of it is uniform, which the compiler does not see through the
+        // table: in vector registers it would spill the k-loop)
+        const auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+        t.ksteps = uniform(t.ksteps);
+        t.tn = uniform(t.tn);
+        t.rows = uniform(t.rows);
+        t.bias = uniform(t.bias);
+        t.base = (int64_t)(((uint64_t)(uint32_t)uniform((int)(t.base >> 32)) << 32) | (uint32_t)uniform((int)t.base));
+        // row groups past an operand are clamped to its last one: those rows of C are not stored
+#pragma unroll
+        for (int r = 0; r < C::kLoLoads; ++r) {
+            const bool isA = C::kWaves * (r + 1) <= C::kGA;
+            const int a = C::kWaves * r + wave;
+            const int row = isA ? min(tm * C::kGA + a, nGA - 1) : min(t.tn * C::kGB + a - C::kGA, nGB - 1);
+            lo[r] = uniform((isA ? lo_a : lo_b) + row * t.ksteps * 1024);
+            sc[r] = uniform((isA ? sc_a : sc_b) + row * kgroups * 256);
+        }
+    };
+    static_assert(C::kLoLoads == C::kScaleLoads && C::kHiLoads == 0, "one offset each per unit");
+    const auto bias_of = [&](const StreamTile &t) {
+        return make_rsrc(bias + (int64_t)(t.bias > 0 ? t.bias : 0) * N, t.bias < 0 ? 0 : (N * 2 + 15) / 16 * 16);
+    };
+    const auto start_tile = [&](const StreamTile &t) {
+        c.ksteps = t.ksteps;
+        c.kgroups = (t.ksteps + 3) / 4;
+        c.kstream = 4 * max(c.kgroups, 1);
+    };
+
+    StreamTile cur, next{};
+    resolve(at, cur, c.lo_row, c.sc_row);
+    start_tile(cur);
+    c.knext = 0;
+    at += step;
+    if (at < stop) {
+        resolve(at, next, c.lo_next, c.sc_next);
+        c.knext = next.ksteps;
+    }
+    v16f acc[C::kMB][C::kMA];
+    v2u_t bias_bits[BIAS ? C::kMB * 4 : 1];
+    if constexpr (BIAS) load_bias<C>(bias_of(cur), cur.tn, wn, lane, bias_bits);
+
+    // as in the ungrouped persistent form: steps 0-2 whole, all landed before the first k-step
+    dma_part<C, 0, 0, 0, 0>(c, 0);
+    dma_part<C, 0, 0, 1, 0>(c, 0);
+    dma_part<C, 1, 1, 0, 0>(c, 1);
+    dma_part<C, 1, 1, 1, 0>(c, 1);
+    dma_part<C, 2, 2, 0, 0>(c, 2);
+    dma_part<C, 2, 2, 1, 0>(c, 2);
+    const Lds l = lds_offsets<C>(wave, lane);
+    Regs<C> r;
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+    __builtin_amdgcn_s_barrier();
+    first_operands<C, 0>(r, l);
+
+    for (;;) {
+        period<C, true, kFreshOps, false, 0>(c, 0, acc, r, l);
+        int k0 = C::kPeriod;
+        for (; k0 + C::kPeriod + 2 < c.ksteps; k0 += C::kPeriod) period<C, false, 0, true, 0>(c, k0, acc, r, l);
+        for (; k0 < c.kstream; k0 += C::kPeriod) period<C, false, 0, false, 0>(c, k0, acc, r, l);
+        if constexpr (BIAS) add_bias<C>(acc, bias_bits);
+        dma_part<C, 2, 2, 1, 0>(c, c.kstream + 2);
+        store_tile_private<C>(acc, 0, cur.tn, cur.rows, N, make_rsrc(Cout + cur.base, kBlob), ldc, wave, hidden(lane));
+        if constexpr (BIAS) {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            load_bias<C>(bias_of(next), next.tn, wn, lane, bias_bits);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (at >= stop) break;
+        at += step;
+        cur = next;
+        start_tile(cur);
+#pragma unroll
+        for (int q = 0; q < C::kLoLoads; ++q) c.lo_row[q] = c.lo_next[q];
+#pragma unroll
+        for (int q = 0; q < C::kScaleLoads; ++q) c.sc_row[q] = c.sc_next[q];
+        c.knext = 0;
+        if (at < stop) {
+            resolve(at, next, c.lo_next, c.sc_next);
+            c.knext = next.ksteps;
+        }
+    }
+    // drain the stores and the trailing (out-of-range) DMAs
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
 // Most tiles of `tile` rows that M rows in `groups` groups and the rows
 // behind the last group can need.
 int64_t max_tiles(int64_t M, int groups, int tile) {
@@ -324,6 +568,31 @@ hipError_t launch_few(const GroupedGemmArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Whether the persistent form takes the product: bf16 output in whole 8-column
+// chunks and 32-bit offsets into both blobs and a tile of C.
+bool stream_fits(const GroupedGemmArgs &a, int64_t a_bytes, int64_t b_bytes) {
+    constexpr int64_t kLimit = (int64_t(1) << 31) - 1;
+    return a.out_dtype == MX_BF16 && a.groups <= kStreamGroups && a_bytes <= kLimit && b_bytes <= kLimit &&
+           256 * a.ldc * 2 <= kLimit && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
+}
+
+hipError_t launch_stream(const GroupedGemmArgs &a, int cus, hipStream_t stream) {
+    using C = Cfg<Fp4Fmt, MainShape>;
+    auto kernel = a.bias ? gemm_grouped_stream_kernel<C, false, true> : gemm_grouped_stream_kernel<C, false, false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)cus), dim3(C::kThreads), 0, stream, a.ends, a.groups, (int)a.M, (int)a.M,
+                       (int)a.N, (int)padded(a.K), 0, (int)cdiv(a.N, C::kBN), a.A, a.As, a.B, a.Bs, a.bias,
+                       static_cast<uint16_t *>(a.C), (int)a.ldc, int64_t(0));
+    return hipGetLastError();
+}
+
+hipError_t launch_wgrad_stream(const GroupedGemmArgs &a, int cus, hipStream_t stream) {
+    using C = Cfg<Fp4Fmt, MainShape>;
+    hipLaunchKernelGGL((gemm_grouped_stream_kernel<C, true, false>), dim3((unsigned)cus), dim3(C::kThreads), 0, stream,
+                       a.ends, a.groups, (int)a.M, (int)a.N, (int)a.K, 0, 0, (int)cdiv(a.K, C::kBN), a.A, a.As, a.B,
+                       a.Bs, a.bias, static_cast<uint16_t *>(a.C), (int)a.ldc, a.group_stride);
+    return hipGetLastError();
+}
+
 template <class S>
 hipError_t launch_wgrad_shape(const GroupedGemmArgs &a, hipStream_t stream) {
     using C = Cfg<Fp4Fmt, S>;
@@ -350,11 +619,23 @@ bool grouped_wgrad_fits(int64_t N, int64_t K, int groups) {
 }
 
 hipError_t launch_gemm_grouped(const GroupedGemmArgs &a, hipStream_t stream) {
-    if (a.M <= 32 * (a.groups < a.M ? a.groups : a.M)) return launch_few(a, stream);
+    const int64_t full = a.groups < a.M ? a.groups : a.M;
+    if (a.M <= 32 * full) return launch_few(a, stream);
+    const int cus = device_cu_count() / kXcds * kXcds;
+    const int64_t bytes = padded(a.K) / 2;
+    if (cus > 0 && a.N % 8 == 0 && a.K > 0 && (a.M / 256 + full / 2) * cdiv(a.N, 256) > cus &&
+        stream_fits(a, (a.M + 15 * full) / 16 * 16 * bytes, a.groups * (cdiv(a.N, 16) * 16) * bytes))
+        return launch_stream(a, cus, stream);
     return a.M >= 128 * (int64_t)a.groups ? launch_shape<MainShape>(a, stream) : launch_shape<TailShape>(a, stream);
 }
 
 hipError_t launch_gemm_grouped_wgrad(const GroupedGemmArgs &a, hipStream_t stream) {
+    const int64_t full = a.groups < a.M ? a.groups : a.M;
+    const int cus = device_cu_count() / kXcds * kXcds;
+    const int64_t bytes = (a.M + 127 * full) / 128 * 64;   // a blob's per row
+    if (cus > 0 && a.K % 8 == 0 && a.groups * cdiv(a.N, 256) * cdiv(a.K, 256) > cus &&
+        stream_fits(a, cdiv(a.N, 16) * 16 * bytes, cdiv(a.K, 16) * 16 * bytes))
+        return launch_wgrad_stream(a, cus, stream);
     return launch_wgrad_shape<MainShape>(a, stream);
 }
 

@@ -212,6 +212,34 @@ def test_product_with_bias(oracle_mod, sizes, N, K):
     run_product(oracle_mod, synth.random_bf16(1, (M, K)), w, ends_of(sizes), synth.random_bf16(3, (len(sizes), N)))
 
 
+MANY = [(i * 29) % 97 if i % 6 else 0 for i in range(75)]          # ragged, some empty
+
+
+@pytest.mark.parametrize("sizes", [MANY, [700, 0, 256, 1, 513, 900, 31, 300], [3000]],
+                         ids=lambda s: "%d_groups_%d_rows" % (len(s), sum(s)))
+@pytest.mark.parametrize("N,K,bias", [(1800, 40, False), (2056, 264, True), (1544, 776, False)])
+def test_product_of_many_tiles(oracle_mod, sizes, N, K, bias):
+    """More output tiles than compute units: workgroups that run from tile to tile, across groups, over the rows in no
+    group, with fewer k-steps than one k-group holds and with several."""
+    if len(sizes) < 10:
+        N, sizes = (6000, sizes) if len(sizes) == 1 else (N + 700, sizes * 2)
+    M = sum(sizes) + 300                                # two tiles of rows in no group
+    w = synth.random_bf16(2, (len(sizes), N, K), std=0.05)
+    b = synth.random_bf16(3, (len(sizes), N)) if bias else None
+    run_product(oracle_mod, synth.random_bf16(1, (M, K)), w, ends_of(sizes), b, "many tiles")
+
+
+@pytest.mark.parametrize("sizes", [MANY, [40, 0, 600, 129, 1300, 1, 0, 512] * 4],
+                         ids=lambda s: "%d_groups_%d_rows" % (len(s), sum(s)))
+@pytest.mark.parametrize("N,K", [(300, 520), (600, 784)])
+def test_wgrad_of_many_tiles(oracle_mod, sizes, N, K):
+    """The same for the weights' gradient, where a tile's length is its group's."""
+    if len(sizes) < 60:
+        N += 300
+    M = sum(sizes) + 2
+    run_wgrad(oracle_mod, synth.random_bf16(N, (M, N), std=1e-3), synth.random_bf16(K, (M, K)), ends_of(sizes), "many")
+
+
 def test_product_propagates_nan_blocks_to_their_rows_only(oracle_mod):
     sizes, N, K = [5, 40, 3], 48, 256
     x, w = synth.random_bf16(1, (48, K)), synth.random_bf16(2, (3, N, K))
