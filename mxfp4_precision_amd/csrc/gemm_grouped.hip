@@ -101,15 +101,15 @@ __global__ __launch_bounds__(C::kThreads) void gemm_grouped_kernel(const int32_t
 // into registers.  A workgroup's tile is 64 rows (or the group's remainder,
 // MA atoms) x 32 columns; its four waves take k-step 4 h + wave of every
 // k-group h, so each reads one byte of the scale dwords that all four load,
-// and their sums are added in wave order through LDS.  kDepth k-groups are
-// in flight per wave.
+// and their sums are added in wave order through LDS.  Up to eight k-groups
+// are in flight per wave.
 constexpr int kFewM = 64, kFewNB = 2, kFewN = 16 * kFewNB;
 
 template <int MA, int DEPTH>
 __device__ __forceinline__ void few_rows_sum(__amdgpu_buffer_rsrc_t rA, __amdgpu_buffer_rsrc_t rAs,
                                              __amdgpu_buffer_rsrc_t rB, __amdgpu_buffer_rsrc_t rBs, int gA0, int nGA,
                                              int gB0, int nGB, int ksteps, int kgroups, int wave, int lane,
-                                             v4f (&acc)[kFewM / 16][kFewNB]) {
+                                             v4f (&acc)[kFewM / 16][kFewNB], int h0 = 0) {
     // atom rows past an operand are clamped to its last one: those results are not stored
     int a_row[MA], b_row[kFewNB];
 #pragma unroll
@@ -117,26 +117,26 @@ __device__ __forceinline__ void few_rows_sum(__amdgpu_buffer_rsrc_t rA, __amdgpu
 #pragma unroll
     for (int j = 0; j < kFewNB; ++j) b_row[j] = min(gB0 + j, nGB - 1);
     const uint32_t lane16 = (uint32_t)lane * 16, lane4 = (uint32_t)lane * 4;
-    for (int h0 = 0; h0 < kgroups; h0 += DEPTH) {
+    for (; h0 + DEPTH <= kgroups; h0 += DEPTH) {
         v4u_t a[DEPTH][MA], b[DEPTH][kFewNB];
         uint32_t as[DEPTH][MA], bs[DEPTH][kFewNB];
 #pragma unroll
         for (int u = 0; u < DEPTH; ++u) {
             const int h = h0 + u, ks = 4 * h + wave;
-            // Past K both read as zeros: the lane offset is out of range on its
-            // own, the scalar one is then 0 (the range check subtracts it from
-            // the range).
-            const bool in = ks < ksteps, sin = h < kgroups;
-            const uint32_t off = in ? lane16 : kOutOfRange, soff = sin ? lane4 : kOutOfRange;
+            // Past K the data read as zeros: the lane offset is out of range on
+            // its own, the scalar one is then 0 (the range check subtracts it
+            // from the range).
+            const bool in = ks < ksteps;
+            const uint32_t off = in ? lane16 : kOutOfRange;
 #pragma unroll
             for (int j = 0; j < kFewNB; ++j) {
                 b[u][j] = __builtin_amdgcn_raw_buffer_load_b128(rB, off, in ? (b_row[j] * ksteps + ks) * 1024 : 0, 0);
-                bs[u][j] = __builtin_amdgcn_raw_buffer_load_b32(rBs, soff, sin ? (b_row[j] * kgroups + h) * 256 : 0, 0);
+                bs[u][j] = __builtin_amdgcn_raw_buffer_load_b32(rBs, lane4, (b_row[j] * kgroups + h) * 256, 0);
             }
 #pragma unroll
             for (int i = 0; i < MA; ++i) {
                 a[u][i] = __builtin_amdgcn_raw_buffer_load_b128(rA, off, in ? (a_row[i] * ksteps + ks) * 1024 : 0, 0);
-                as[u][i] = __builtin_amdgcn_raw_buffer_load_b32(rAs, soff, sin ? (a_row[i] * kgroups + h) * 256 : 0, 0);
+                as[u][i] = __builtin_amdgcn_raw_buffer_load_b32(rAs, lane4, (a_row[i] * kgroups + h) * 256, 0);
             }
         }
 #pragma unroll
@@ -152,6 +152,9 @@ __device__ __forceinline__ void few_rows_sum(__amdgpu_buffer_rsrc_t rA, __amdgpu
                                                                                  Fp4Fmt::kFa, 0, sb, 0, sa);
                 }
     }
+    // the k-groups left over, half as many at a time
+    if constexpr (DEPTH > 1)
+        few_rows_sum<MA, DEPTH / 2>(rA, rAs, rB, rBs, gA0, nGA, gB0, nGB, ksteps, kgroups, wave, lane, acc, h0);
 }
 
 template <bool OUT_BF16, bool BIAS>
@@ -618,23 +621,42 @@ bool grouped_wgrad_fits(int64_t N, int64_t K, int groups) {
     return groups * (cdiv(N, 128) * cdiv(K, 128)) < kMaxBlocks;
 }
 
+// Which form takes a product, by the tiles that M rows spread evenly over the
+// groups with rows make (the real spread is known on the device only).
+// Measured on MI355X in us, few rows / 128x128 / persistent 256x256:
+//   64 groups of 4, N 2048, K 4096    52 /  75 /  78
+//   64 groups of 32                   68 /  77 /  79
+//   64 groups of 64                   93 /  81 /  80
+//   4 groups of 256, N 1200, K 1024  5.5 / 6.5 / 9.9
+//   12 groups of 64                  5.2 / 6.0 / 9.7
+//   12 groups of 128                 8.5 / 7.1 / 9.9
+//   12 groups of 512                   - /  17 /  14
+//   64 groups of 128                  34 /  22 /  24
+//   64 groups of 256                  58 /  34 /  31
+// The few-rows form therefore for groups of at most 32 rows, or where its
+// small tiles are no more than the CUs hold at once; else 128x128 tiles until
+// they number 1.3 per CU and groups hold 192 rows.
 hipError_t launch_gemm_grouped(const GroupedGemmArgs &a, hipStream_t stream) {
     const int64_t full = a.groups < a.M ? a.groups : a.M;
-    if (a.M <= 32 * full) return launch_few(a, stream);
     const int cus = device_cu_count() / kXcds * kXcds;
+    const auto tiles = [&](int bm, int bn) { return (a.M + bm * full / 2) / bm * cdiv(a.N, bn); };
+    if (a.M <= 32 * full || 10 * tiles(kFewM, kFewN) <= 26 * cus) return launch_few(a, stream);
+    if (10 * tiles(128, 128) <= 13 * cus || a.M < 192 * full) return launch_shape<TailShape>(a, stream);
     const int64_t bytes = padded(a.K) / 2;
-    if (cus > 0 && a.N % 8 == 0 && a.K > 0 && (a.M / 256 + full / 2) * cdiv(a.N, 256) > cus &&
+    if (cus > 0 && a.N % 8 == 0 && a.K > 0 &&
         stream_fits(a, (a.M + 15 * full) / 16 * 16 * bytes, a.groups * (cdiv(a.N, 16) * 16) * bytes))
         return launch_stream(a, cus, stream);
-    return a.M >= 128 * (int64_t)a.groups ? launch_shape<MainShape>(a, stream) : launch_shape<TailShape>(a, stream);
+    return launch_shape<MainShape>(a, stream);
 }
 
+// 128x128 tiles while they number at most 1.3 per CU: 4 groups of 1200 x 1024
+// 6.8 us (persistent 8.3), 12 groups of it 12.8 (10.8).
 hipError_t launch_gemm_grouped_wgrad(const GroupedGemmArgs &a, hipStream_t stream) {
     const int64_t full = a.groups < a.M ? a.groups : a.M;
     const int cus = device_cu_count() / kXcds * kXcds;
+    if (10 * a.groups * cdiv(a.N, 128) * cdiv(a.K, 128) <= 13 * cus) return launch_wgrad_shape<TailShape>(a, stream);
     const int64_t bytes = (a.M + 127 * full) / 128 * 64;   // a blob's per row
-    if (cus > 0 && a.K % 8 == 0 && a.groups * cdiv(a.N, 256) * cdiv(a.K, 256) > cus &&
-        stream_fits(a, cdiv(a.N, 16) * 16 * bytes, cdiv(a.K, 16) * 16 * bytes))
+    if (cus > 0 && a.K % 8 == 0 && stream_fits(a, cdiv(a.N, 16) * 16 * bytes, cdiv(a.K, 16) * 16 * bytes))
         return launch_wgrad_stream(a, cus, stream);
     return launch_wgrad_shape<MainShape>(a, stream);
 }
