@@ -20,10 +20,17 @@
 // for training.  A positive sqrt(v) keeps at least the smallest code: at 0
 // the next update would be divided by eps.
 //
-// Bound by memory (26 bytes per element with fp32 states, 14.125 with 8-bit
-// ones at fp32 parameters and bf16 gradients).  A lane owns 8 consecutive
-// elements, so a block's largest value is found in its 4 lanes with two DPP
-// quad permutes.
+// A lane owns 8 consecutive elements, so a block's largest value is found in
+// its 4 lanes with two DPP quad permutes.  Measured on MI355X:
+//  - fp32 states, fp32 parameters, bf16 gradients and copy (28 bytes an
+//    element), 76M elements: 395 us, 5.4 TB/s; bound by memory (a 4 GiB copy
+//    moves 4.8 TB/s).  Plain fp32 loads, as the lines are written again at
+//    once: 418 us with non-temporal ones.
+//  - MXFP8 states, bf16 parameters and gradients, stochastic (10.1 bytes), 201M
+//    elements: 381 us, 5.3 TB/s, memory and arithmetic about even (65 vector
+//    instructions an element, 13 of them Philox).  The earlier forms of the
+//    decode (ldexp and a NaN select per value), the encode (codes masked and
+//    shifted one by one) and the square root took 434 us.
 
 #include "mx_internal.h"
 
@@ -52,14 +59,15 @@ __device__ __forceinline__ void philox(uint32_t (&c)[4], uint32_t k0, uint32_t k
     }
 }
 
-// Eight elements at p + i, of which the first `left` exist (the others read 0).
-template <bool F32>
+// Eight elements at p + i, of which the first `left` exist (the others read
+// 0); FULL: all eight do.
+template <bool FULL, bool F32>
 __device__ __forceinline__ void load8(const void *p, int64_t i, int left, float (&v)[8]) {
     if constexpr (F32) {
         const float *s = static_cast<const float *>(p) + i;
-        if (left >= 8) {
-            const f4_t a = __builtin_nontemporal_load(reinterpret_cast<const f4_t *>(s));
-            const f4_t b = __builtin_nontemporal_load(reinterpret_cast<const f4_t *>(s) + 1);
+        if (FULL || left >= 8) {
+            const f4_t a = *reinterpret_cast<const f4_t *>(s);
+            const f4_t b = *(reinterpret_cast<const f4_t *>(s) + 1);
 #pragma unroll
             for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
         } else {
@@ -68,7 +76,7 @@ __device__ __forceinline__ void load8(const void *p, int64_t i, int left, float 
         }
     } else {
         const uint16_t *s = static_cast<const uint16_t *>(p) + i;
-        if (left >= 8) {
+        if (FULL || left >= 8) {
             const u4_t a = __builtin_nontemporal_load(reinterpret_cast<const u4_t *>(s));
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -82,11 +90,11 @@ __device__ __forceinline__ void load8(const void *p, int64_t i, int left, float 
     }
 }
 
-template <bool F32>
+template <bool FULL, bool F32>
 __device__ __forceinline__ void store8(void *p, int64_t i, int left, const float (&v)[8]) {
     if constexpr (F32) {
         float *s = static_cast<float *>(p) + i;
-        if (left >= 8) {
+        if (FULL || left >= 8) {
             __builtin_nontemporal_store(f4_t{v[0], v[1], v[2], v[3]}, reinterpret_cast<f4_t *>(s));
             __builtin_nontemporal_store(f4_t{v[4], v[5], v[6], v[7]}, reinterpret_cast<f4_t *>(s) + 1);
         } else {
@@ -100,7 +108,7 @@ __device__ __forceinline__ void store8(void *p, int64_t i, int left, const float
         for (int e = 0; e < 4; ++e)
             w[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2_t{v[2 * e], v[2 * e + 1]}), bf2_t));
         uint16_t *s = static_cast<uint16_t *>(p) + i;
-        if (left >= 8) {
+        if (FULL || left >= 8) {
             __builtin_nontemporal_store(u4_t{w[0], w[1], w[2], w[3]}, reinterpret_cast<u4_t *>(s));
         } else {
 #pragma unroll
@@ -111,13 +119,14 @@ __device__ __forceinline__ void store8(void *p, int64_t i, int left, const float
 }
 
 // Eight E4M3 codes at p + i (a multiple of 8) and their block's scale byte.
+template <bool FULL>
 __device__ __forceinline__ void load_codes(const uint8_t *p, const uint8_t *scale, int64_t i, int left, u2_t &w,
                                            uint32_t &c) {
     w = u2_t{0u, 0u};
     c = 0;
-    if (left <= 0) return;
+    if (!FULL && left <= 0) return;
     c = scale[i / 32];
-    if (left >= 8) {
+    if (FULL || left >= 8) {
         w = __builtin_nontemporal_load(reinterpret_cast<const u2_t *>(p + i));
     } else {
 #pragma unroll
@@ -126,18 +135,19 @@ __device__ __forceinline__ void load_codes(const uint8_t *p, const uint8_t *scal
     }
 }
 
-// The values they stand for: E4M3 times 2^(c - 127), NaN for c = 0xFF.
+// The values they stand for: E4M3 times 2^(c - 127), NaN for c = 0xFF.  The
+// scale is an fp32 number for every c < 0xFF (2^-127 a subnormal one) and the
+// product exact.
 __device__ __forceinline__ void decode8(u2_t w, uint32_t c, float (&v)[8]) {
+    const float scale = c == 0xFFu ? __uint_as_float(0x7FC00000u)
+                                   : __builtin_ldexpf(__uint_as_float(0x00400000u), (int)c);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const f2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[h], false);
         const f2_t b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[h], true);
-        v[4 * h] = a[0]; v[4 * h + 1] = a[1]; v[4 * h + 2] = b[0]; v[4 * h + 3] = b[1];
+        v[4 * h] = a[0] * scale; v[4 * h + 1] = a[1] * scale;
+        v[4 * h + 2] = b[0] * scale; v[4 * h + 3] = b[1] * scale;
     }
-    const int e = c == 0xFFu ? 0 : (int)c - 127;
-    const float nan = __uint_as_float(0x7FC00000u);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = c == 0xFFu ? nan : __builtin_ldexpf(v[k], e);
 }
 
 // A block's scale byte from its largest magnitude as an fp32 pattern: the
@@ -157,29 +167,47 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v) {
     return max_u(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
 }
 
+// Byte 3 of four words.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __builtin_amdgcn_perm(b, a, 0x0C0C0703u) | __builtin_amdgcn_perm(d, c, 0x07030C0Cu);
+}
+
 // Eight values -> E4M3 codes under scale byte c.  u = |x| 2^(7 - c) as an
 // fp32 pattern has E4M3's fields on top (its subnormal step falls on the fp32
 // subnormal grid): the code is u >> 20, plus 1 when the 16 bits below it
-// exceed what the random bits leave (SR) or by the nearest-even rule.
+// exceed what the random bits leave (SR) or by the nearest-even rule.  It is
+// formed in the top byte of u << 4, where one permute gathers two codes.
+// ROOT: values >= 0; its random bits are the words' upper halves.
 template <bool SR, bool ROOT>
 __device__ __forceinline__ u2_t encode8(const float (&x)[8], uint32_t c, const uint32_t (&bits)[8]) {
-    u2_t w = {0u, 0u};
+    uint32_t s[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const uint32_t xb = __float_as_uint(x[e]);
-        const uint32_t u = __float_as_uint(__builtin_ldexpf(__uint_as_float(xb & 0x7FFFFFFFu), 7 - (int)c));
-        uint32_t code = SR ? (u + ((ROOT ? bits[e] >> 16 : bits[e] & 0xFFFFu) << 4)) >> 20
-                           : (u + 0x7FFFFu + ((u >> 20) & 1u)) >> 20;
-        code = code < 126u ? code : 126u;
-        if (ROOT) code = x[e] > 0.0f && code == 0u ? 1u : code;
-        else code |= (xb >> 24) & 0x80u;
-        w[e >> 2] |= code << (8 * (e & 3));
+        const uint32_t u = __float_as_uint(__builtin_ldexpf(__builtin_fabsf(x[e]), 7 - (int)c));
+        uint32_t v;
+        if constexpr (SR)   // 16 random bits at bits 8..23
+            v = (u << 4) + __builtin_amdgcn_perm(bits[e], bits[e], ROOT ? 0x0C03020Cu : 0x0C01000Cu);
+        else
+            v = (u + 0x7FFFFu + ((u >> 20) & 1u)) << 4;
+        v = v < 0x7EFFFFFFu ? v : 0x7EFFFFFFu;
+        if constexpr (ROOT) {   // a positive value keeps at least the smallest code
+            const uint32_t least = x[e] > 0.0f ? 1u << 24 : 0u;
+            v = v > least ? v : least;
+        }
+        s[e] = v;
+    }
+    u2_t w = {top_bytes(s[0], s[1], s[2], s[3]), top_bytes(s[4], s[5], s[6], s[7])};
+    if constexpr (!ROOT) {
+        const auto bit = [&](int e) { return __float_as_uint(x[e]); };
+        w[0] |= top_bytes(bit(0), bit(1), bit(2), bit(3)) & 0x80808080u;
+        w[1] |= top_bytes(bit(4), bit(5), bit(6), bit(7)) & 0x80808080u;
     }
     return c == 0xFFu ? u2_t{0u, 0u} : w;
 }
 
+template <bool FULL>
 __device__ __forceinline__ void store_codes(uint8_t *p, int64_t i, int left, u2_t w) {
-    if (left >= 8) {
+    if (FULL || left >= 8) {
         __builtin_nontemporal_store(w, reinterpret_cast<u2_t *>(p + i));
     } else {
 #pragma unroll
@@ -188,43 +216,53 @@ __device__ __forceinline__ void store_codes(uint8_t *p, int64_t i, int left, u2_
     }
 }
 
-template <bool P32, bool G32, bool S8, bool SR>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwBatch b) {
+// Square roots, rounded to nearest.  The compiler's own sequence scales small
+// arguments and tests for special ones; where a wave has none of either
+// (arguments in [2^-96, 2^96]) v_sqrt_f32, off by at most one step, and the
+// residuals of its two neighbours do.
+__device__ __forceinline__ void sqrt8(const float (&v)[8], float (&root)[8]) {
 #pragma clang fp contract(off)
-    // the tensor of this workgroup's chunk
-    int t = 0;
-    {
-        int lo = 0, hi = b.count - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (blockIdx.x < b.t[mid].chunk_end) hi = mid;
-            else lo = mid + 1;
-        }
-        t = lo;
+    uint32_t lo = ~0u, hi = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t b = __float_as_uint(v[e]);
+        lo = b < lo ? b : lo;
+        hi = max_u(hi, b);
     }
-    const AdamwItem &it = b.t[t];
-    const uint32_t first = t ? b.t[t - 1].chunk_end : 0u;
-    const int64_t i = (int64_t)(blockIdx.x - first) * kChunk + (int64_t)threadIdx.x * kLaneElems;
-    const int64_t l = it.numel - i;
-    const int left = l < 0 ? 0 : (l > 8 ? 8 : (int)l);
-    mx_adamw_step h = b.step;
-    if (b.dev_step) h = *b.dev_step;
+    if (__builtin_amdgcn_ballot_w64(lo < 0x0F800000u || hi > 0x6F800000u) == 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float s = __builtin_amdgcn_sqrtf(v[e]);
+            const float below = __uint_as_float(__float_as_uint(s) - 1u), above = __uint_as_float(__float_as_uint(s) + 1u);
+            float r = __builtin_fmaf(-below, s, v[e]) <= 0.0f ? below : s;
+            root[e] = __builtin_fmaf(-above, s, v[e]) > 0.0f ? above : r;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) root[e] = __builtin_sqrtf(v[e]);
+    }
+}
 
+// This lane's eight elements from i on, of which `left` exist.
+template <bool FULL, bool P32, bool G32, bool S8, bool SR>
+__device__ __forceinline__ void update8(const AdamwBatch &b, const AdamwItem &it, const mx_adamw_step &h, int64_t i,
+                                        int left) {
+#pragma clang fp contract(off)
     float p[8], g[8], m[8], v[8];
-    load8<G32>(it.grad, i, left, g);
-    load8<P32>(it.param, i, left, p);
+    load8<FULL, G32>(it.grad, i, left, g);
+    load8<FULL, P32>(it.param, i, left, p);
     if constexpr (S8) {
         u2_t wm, wv;
         uint32_t cm, cv;
-        load_codes(static_cast<const uint8_t *>(it.m), it.ms, i, left, wm, cm);
-        load_codes(static_cast<const uint8_t *>(it.v), it.vs, i, left, wv, cv);
+        load_codes<FULL>(static_cast<const uint8_t *>(it.m), it.ms, i, left, wm, cm);
+        load_codes<FULL>(static_cast<const uint8_t *>(it.v), it.vs, i, left, wv, cv);
         decode8(wm, cm, m);
         decode8(wv, cv, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = v[e] * v[e];
     } else {
-        load8<true>(it.m, i, left, m);
-        load8<true>(it.v, i, left, v);
+        load8<FULL, true>(it.m, i, left, m);
+        load8<FULL, true>(it.v, i, left, v);
     }
     float root[8];
 #pragma unroll
@@ -232,18 +270,21 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwBatch b) {
         const float gg = g[e] * h.grad_scale;
         m[e] = m[e] * b.beta1 + gg * b.one_minus_beta1;
         v[e] = v[e] * b.beta2 + (gg * gg) * b.one_minus_beta2;
-        root[e] = __builtin_sqrtf(v[e]);
-        p[e] = p[e] * h.decay - (m[e] / (root[e] * h.root_factor + b.eps)) * h.step_size;
     }
-    store8<P32>(it.param, i, left, p);
-    if (it.copy) store8<false>(it.copy, i, left, p);
+    sqrt8(v, root);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        p[e] = p[e] * h.decay - (m[e] / (root[e] * h.root_factor + b.eps)) * h.step_size;
+    store8<FULL, P32>(it.param, i, left, p);
+    if (it.copy) store8<FULL, false>(it.copy, i, left, p);
     if constexpr (S8) {
         uint32_t am = 0, av = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             // elements past the end: 0 in m and v, whatever eps does to them
+            // (a root's sign bit is set in a NaN only, which sorts on top either way)
             am = max_u(am, __float_as_uint(m[e]) & 0x7FFFFFFFu);
-            av = max_u(av, __float_as_uint(root[e]) & 0x7FFFFFFFu);
+            av = max_u(av, __float_as_uint(root[e]));
         }
         const uint32_t cm = scale_of(block_max(am)), cv = scale_of(block_max(av));
         uint32_t bits[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
@@ -257,15 +298,41 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwBatch b) {
                 for (int e = 0; e < 4; ++e) bits[4 * q + e] = c[e];
             }
         }
-        store_codes(static_cast<uint8_t *>(it.m), i, left, encode8<SR, false>(m, cm, bits));
-        store_codes(static_cast<uint8_t *>(it.v), i, left, encode8<SR, true>(root, cv, bits));
-        if (left > 0 && (threadIdx.x & 3) == 0) {
+        store_codes<FULL>(static_cast<uint8_t *>(it.m), i, left, encode8<SR, false>(m, cm, bits));
+        store_codes<FULL>(static_cast<uint8_t *>(it.v), i, left, encode8<SR, true>(root, cv, bits));
+        if ((FULL || left > 0) && (threadIdx.x & 3) == 0) {
             it.ms[i / 32] = (uint8_t)cm;
             it.vs[i / 32] = (uint8_t)cv;
         }
     } else {
-        store8<true>(it.m, i, left, m);
-        store8<true>(it.v, i, left, v);
+        store8<FULL, true>(it.m, i, left, m);
+        store8<FULL, true>(it.v, i, left, v);
+    }
+}
+
+template <bool P32, bool G32, bool S8, bool SR>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwBatch b) {
+    // the tensor of this workgroup's chunk
+    int t = 0;
+    {
+        int lo = 0, hi = b.count - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (blockIdx.x < b.t[mid].chunk_end) hi = mid;
+            else lo = mid + 1;
+        }
+        t = lo;
+    }
+    const AdamwItem &it = b.t[t];
+    const int64_t first = (int64_t)(blockIdx.x - (t ? b.t[t - 1].chunk_end : 0u)) * kChunk;
+    mx_adamw_step h = b.step;
+    if (b.dev_step) h = *b.dev_step;
+    const int64_t i = first + (int64_t)threadIdx.x * kLaneElems;
+    if (first + kChunk <= it.numel) {
+        update8<true, P32, G32, S8, SR>(b, it, h, i, 8);
+    } else {
+        const int64_t l = it.numel - i;
+        update8<false, P32, G32, S8, SR>(b, it, h, i, l < 0 ? 0 : (l > 8 ? 8 : (int)l));
     }
 }
 
