@@ -104,6 +104,11 @@ def adamw_table(rows):
     return (mx_adamw_tensor * max(len(rows), 1))(*rows)
 
 
+try:
+    from . import _marshal      # converts the arguments of the grouped calls (csrc/marshal.cpp)
+except ImportError:
+    _marshal = None             # the same conversions in Python
+
 _lib = None
 
 
@@ -151,6 +156,10 @@ def lib() -> ctypes.CDLL:
     for name in EXPORTED:
         if name not in ("mx_device_supported", "mx_status_string", "mx_last_error"):
             getattr(L, name).restype = i32     # mx_status
+    if _marshal is not None:
+        address = lambda f: ctypes.cast(f, vp).value  # noqa: E731
+        _marshal.bind(address(L.mx_quantize_grouped), address(L.mx_gemm_a4w4_grouped),
+                      address(L.mx_gemm_a4w4_grouped_wgrad), _dptr, _i32ptr, _stream)
     _lib = L
     return L
 
@@ -312,23 +321,37 @@ def mx_grouped_blob_bytes(M: int, N: int, groups: int) -> Tuple[int, int, int, i
 
 def mx_quantize_grouped(x, x_rows: int, N: int, ldx: int, row_index, M: int, group_ends, groups: int, row_opts,
                         col_opts, layout: int, q_row, s_row, q_col=None, s_col=None, stream=None):
-    _check(lib().mx_quantize_grouped(_dptr(x), x_rows, N, ldx, _i32ptr(row_index, M), M, _i32ptr(group_ends, groups), groups,
-                                     _opts(row_opts), _opts(col_opts), layout, _dptr(q_row), _dptr(s_row),
-                                     _dptr(q_col), _dptr(s_col), _stream(stream)))
+    L = lib()
+    if _marshal is not None:
+        _check(_marshal.quantize_grouped(x, x_rows, N, ldx, row_index, M, group_ends, groups, row_opts, col_opts,
+                                         layout, q_row, s_row, q_col, s_col, stream))
+        return
+    _check(L.mx_quantize_grouped(_dptr(x), x_rows, N, ldx, _i32ptr(row_index, M), M, _i32ptr(group_ends, groups),
+                                 groups, _opts(row_opts), _opts(col_opts), layout, _dptr(q_row), _dptr(s_row),
+                                 _dptr(q_col), _dptr(s_col), _stream(stream)))
 
 
 def mx_gemm_a4w4_grouped(M: int, N: int, K: int, group_ends, groups: int, A, A_scale, B, B_scale, layout: int,
                          out_dtype: int, bias, C, ldc: int, stream=None):
-    _check(lib().mx_gemm_a4w4_grouped(M, N, K, _i32ptr(group_ends, groups), groups, _dptr(A), _dptr(A_scale), _dptr(B),
-                                      _dptr(B_scale), layout, out_dtype, _dptr(bias), _dptr(C), ldc,
-                                      _stream(stream)))
+    L = lib()
+    if _marshal is not None:
+        _check(_marshal.gemm_grouped(M, N, K, group_ends, groups, A, A_scale, B, B_scale, layout, out_dtype, bias, C,
+                                     ldc, stream))
+        return
+    _check(L.mx_gemm_a4w4_grouped(M, N, K, _i32ptr(group_ends, groups), groups, _dptr(A), _dptr(A_scale), _dptr(B),
+                                  _dptr(B_scale), layout, out_dtype, _dptr(bias), _dptr(C), ldc, _stream(stream)))
 
 
 def mx_gemm_a4w4_grouped_wgrad(M: int, N: int, K: int, group_ends, groups: int, A, A_scale, B, B_scale, layout: int,
                                out_dtype: int, C, ldc: int, group_stride: int, stream=None):
-    _check(lib().mx_gemm_a4w4_grouped_wgrad(M, N, K, _i32ptr(group_ends, groups), groups, _dptr(A), _dptr(A_scale), _dptr(B),
-                                            _dptr(B_scale), layout, out_dtype, _dptr(C), ldc, group_stride,
-                                            _stream(stream)))
+    L = lib()
+    if _marshal is not None:
+        _check(_marshal.gemm_grouped_wgrad(M, N, K, group_ends, groups, A, A_scale, B, B_scale, layout, out_dtype, C,
+                                           ldc, group_stride, stream))
+        return
+    _check(L.mx_gemm_a4w4_grouped_wgrad(M, N, K, _i32ptr(group_ends, groups), groups, _dptr(A), _dptr(A_scale),
+                                        _dptr(B), _dptr(B_scale), layout, out_dtype, _dptr(C), ldc, group_stride,
+                                        _stream(stream)))
 
 
 def mx_adamw(tensors, count: int, opts: mx_adamw_opts, stream=None):

@@ -9,6 +9,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +19,8 @@ LIB = os.path.join(HERE, "libmxfp4.so")
 SOURCES = ["api.cpp", "layout.cpp", "quantize.hip", "quantize_fp8.hip", "gemm.hip", "gemm_grouped.hip",
            "adamw.hip", "convert.hip", "dequantize.hip", "measure.hip"]
 ARCH = "gfx950"
+# The Python extension that converts the arguments of the hottest calls (host code).
+MARSHAL = os.path.join(HERE, "_marshal.so")
 
 
 def hipcc() -> str:
@@ -49,7 +52,7 @@ def _compile(src: str) -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libmxfp4.so next to this file."""
+    """Compile every source, link libmxfp4.so next to this file and build the argument marshalling extension."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         objs = list(ex.map(_compile, SOURCES))
@@ -59,6 +62,12 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed: %s\n%s\n%s" % (" ".join(cmd), r.stdout, r.stderr))
     os.replace(tmp, LIB)
+    cmd = [hipcc()] + common_flags() + ["-shared", "-I", sysconfig.get_paths()["include"],
+                                        os.path.join(CSRC, "marshal.cpp"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("compile failed: %s\n%s\n%s" % (" ".join(cmd), r.stdout, r.stderr))
+    os.replace(tmp, MARSHAL)
     if verbose:
         print("built", LIB)
     return LIB

@@ -31,6 +31,14 @@ def status(fn, *args):
         return e.status
 
 
+@pytest.fixture(params=["extension", "ctypes"])
+def binding(request, monkeypatch):
+    """Both conversions of the grouped calls' arguments."""
+    if request.param == "ctypes":
+        monkeypatch.setattr(mx, "_marshal", None)
+    assert (mx._marshal is None) == (request.param == "ctypes"), "build() makes the extension"
+
+
 @pytest.mark.parametrize("M,N,groups", [(0, 5, 3), (1, 1, 1), (1, 40, 64), (300, 200, 7), (1000, 129, 1000),
                                         (4096, 512, 5)])
 def test_blob_bytes_hold_every_split(oracle_mod, M, N, groups):
@@ -58,7 +66,7 @@ def test_blob_bytes_hold_every_split(oracle_mod, M, N, groups):
     assert status(mx.mx_grouped_blob_bytes, 4, 4, 0) == INVALID
 
 
-def test_quantize_grouped_refusals():
+def test_quantize_grouped_refusals(binding):
     o = mx.quant_opts()
 
     def call(**kw):
@@ -82,7 +90,7 @@ def test_quantize_grouped_refusals():
     assert call(M=0) == mx.MX_SUCCESS and call(N=0) == mx.MX_SUCCESS
 
 
-def test_grouped_gemm_refusals():
+def test_grouped_gemm_refusals(binding):
     def call(**kw):
         a = dict(M=9, N=16, K=40, ends=A16, groups=2, A=A16, As=A16, B=A16, Bs=A16, layout=T, dt=mx.MX_BF16, bias=0,
                  C=A16, ldc=16)
@@ -105,7 +113,7 @@ def test_grouped_gemm_refusals():
     assert call(M=0) == mx.MX_SUCCESS and call(N=0) == mx.MX_SUCCESS
 
 
-def test_grouped_wgrad_refusals():
+def test_grouped_wgrad_refusals(binding):
     def call(**kw):
         a = dict(M=9, N=16, K=40, ends=A16, groups=2, A=A16, As=A16, B=A16, Bs=A16, layout=T, dt=mx.MX_BF16, C=A16,
                  ldc=40, stride=640)
@@ -125,7 +133,40 @@ def test_grouped_wgrad_refusals():
     assert call(N=0, stride=0) == mx.MX_SUCCESS and call(K=0) == mx.MX_SUCCESS
 
 
-def test_int32_tensors_only():
+def test_argument_conversions(binding):
+    """Addresses, None, integers, structures and streams arrive; anything else is refused with an error."""
+    torch = pytest.importorskip("torch")
+    quant = [A16, 9, 16, 16, A16, 9, A16, 2, mx.quant_opts(), None, T, A16, A16, A16, A16, 7]
+    gemm = [9, 16, 40, A16, 2, A16, A16, A16, A16, T, mx.MX_BF16, 0, A16, 16, 7]
+    wgrad = [9, 16, 40, A16, 2, A16, A16, A16, A16, T, mx.MX_BF16, A16, 40, 640, 7]
+    tensor = torch.zeros(64, dtype=torch.int32)
+    for fn, args, pointers in ((mx.mx_quantize_grouped, quant, (0, 4, 6, 11, 12, 13, 14)),
+                               (mx.mx_gemm_a4w4_grouped, gemm, (3, 5, 6, 7, 8, 11, 12)),
+                               (mx.mx_gemm_a4w4_grouped_wgrad, wgrad, (3, 5, 6, 7, 8, 11))):
+        assert status(fn, *args) == mx.MX_ERR_DEVICE_UNSUPPORTED
+        for i in range(len(args) - 1):
+            for bad in ("text", 1.5, object()):
+                with pytest.raises((TypeError, ctypes.ArgumentError)):
+                    fn(*[bad if k == i else a for k, a in enumerate(args)])
+        for i in pointers:
+            with pytest.raises(TypeError):                # a host tensor
+                fn(*[tensor if k == i else a for k, a in enumerate(args)])
+        with pytest.raises(TypeError):
+            fn(*args[:-5])
+        with pytest.raises((TypeError, AttributeError)):
+            fn(*args[:-1], object())
+
+        class Stream:
+            cuda_stream = 7
+        assert status(fn, *args[:-1], Stream()) == mx.MX_ERR_DEVICE_UNSUPPORTED
+        # the last status text is this call's own
+        with pytest.raises(mx.MXError, match="gfx000"):
+            fn(*args)
+    with pytest.raises((TypeError, ctypes.ArgumentError)):
+        mx.mx_quantize_grouped(*[mx.mx_adamw_step() if k == 8 else a for k, a in enumerate(quant)])
+
+
+def test_int32_tensors_only(binding):
     torch = pytest.importorskip("torch")
     for bad in (torch.zeros(4, dtype=torch.int64), torch.zeros(8, dtype=torch.int32)[::2],
                 torch.zeros(1, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)):
