@@ -1223,11 +1223,21 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int lane) {
     exchange(w[1], w[3], lane & 2, by2);
 }
 
+constexpr int kEarlyIndex = 256;
+
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a, uint32_t chunks) {
     const int lane = threadIdx.x & 63;
     const uint32_t id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int unit = (int)(id / chunks), chunk = (int)(id % chunks);
     int start = 0, rows = 0, before = 0;   // the unit's group, and the units before it
+    // a short index is read along with the ends instead of after them
+    __shared__ int32_t s_index[4][kEarlyIndex];
+    const bool early = a.row_index && a.M <= kEarlyIndex;
+    if (early) {
+#pragma unroll
+        for (int i = 0; i < kEarlyIndex; i += 64)
+            if (i + lane < a.M) s_index[threadIdx.x >> 6][i + lane] = a.row_index[i + lane];
+    }
     {
         GroupCarry c;
         bool found = false;
@@ -1255,7 +1265,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a, uint32_
         int64_t at = (int64_t)start + r;
         bool real = r < rows;
         if (a.row_index) {
-            at = real ? a.row_index[at] : -1;
+            at = real ? (early ? s_index[threadIdx.x >> 6][at] : a.row_index[at]) : -1;
             real = at >= 0 && at < a.x_rows;
         }
         src[t] = real ? a.x + at * a.ldx : nullptr;
@@ -1264,18 +1274,25 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a, uint32_
     for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const int64_t j = col0 + 128 * m;
             d[m][t] = v4u_t{0u, 0u, 0u, 0u};
-            if (src[t]) {
-                if (j + 8 <= a.N) {
-                    d[m][t] = *reinterpret_cast<const v4u_t *>(src[t] + j);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 7; ++e)
-                        if (j + e < a.N) d[m][t][e >> 1] |= (uint32_t)src[t][j + e] << (16 * (e & 1));
-                }
-            }
+            if (src[t] && col0 + 128 * m + 8 <= a.N) d[m][t] = *reinterpret_cast<const v4u_t *>(src[t] + col0 + 128 * m);
         }
+    // the 8 columns that N ends in
+    if (a.N % 8 != 0 && (uint32_t)(a.N / 512) == (uint32_t)chunk) {
+        const int64_t j = a.N & ~int64_t(7);
+        const int atom = (int)(j % 512) / 128;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (!src[t] || (lane & 15) != (int)(j % 128) / 8) continue;
+            v4u_t v = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (j + e < a.N) v[e >> 1] |= (uint32_t)src[t][j + e] << (16 * (e & 1));
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                if (m == atom) d[m][t] = v;
+        }
+    }
     const int64_t ksteps = a.N_pad / 128, kgroups = cdiv(a.N_pad, 512);
     const int slot = 4 * (lane & 3) + (lane >> 4) + 16 * ((lane & 15) >> 2);   // row + 16 * block of the stores
     uint32_t scales[4] = {0u, 0u, 0u, 0u};
@@ -1308,6 +1325,183 @@ int64_t quantize_rows_blocks(const QuantArgs &a) {
     return cdiv((a.M + 15 * full) / 16 * cdiv(a.N_pad, 512), 4);
 }
 
+// Both blobs of grouped rows in 128-row x 32-column tiles, for inputs whose
+// 128 x 128 tiles would leave CUs idle: there a wave of quantize_kernel is
+// alone on its SIMD with 64 elements a lane, and the launch takes as long as
+// that wave's instructions (600 x 1024 in 8 groups: 7.5 us, 9.8 with
+// stochastic rounding).  Here a lane holds 16 elements, rows 2 q, 2 q + 1 and
+// columns 8 c .. 8 c + 7 of its wave's 32 x 32 (c = lane % 4, q = lane / 4):
+// row blocks are quads of lanes, column blocks all lanes of one c, and every
+// 16-byte slice of either blob lies in one workgroup.  No Hadamard transform.
+template <int CTL>
+__device__ __forceinline__ uint32_t dpp_pk_max(uint32_t v) {
+    return pk_umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTL, 0xF, 0xF, false));
+}
+// Maximum (of 16-bit halves) over the lanes that differ in bits 2..5.
+__device__ __forceinline__ uint32_t max_over_rows(uint32_t v) {
+    v = dpp_pk_max<0x128>(dpp_pk_max<0x124>(v));   // row_ror:4, row_ror:8
+    return lane_max<32, true>(lane_max<16, true>(v));
+}
+
+template <bool ROW_SR, bool COL_SR>
+__global__ __launch_bounds__(256) void quantize_narrow_kernel(QuantArgs a) {
+    __shared__ __attribute__((aligned(16))) uint8_t s_row[128 * 16], s_col[32 * 64];
+    __shared__ __attribute__((aligned(4))) uint8_t s_row_scale[128], s_col_scale[32 * 4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = lane & 3, q = lane >> 2;
+    GroupPos p;
+    const int tile = (int)(blockIdx.y + a.row_tile0);
+    if (!find_tile<kTileRows>(a.ends, a.groups, (int)a.M, [&](int) { return tile; }, p)) return;
+    if (p.group >= a.groups) return;   // rows in no group
+    const int tile_row = p.tile * kTileRows;
+    const int r_loc = 32 * wave + 2 * q;               // the lane's first row in the tile
+    const int64_t col0 = (int64_t)blockIdx.x * 32, j0 = col0 + 8 * c;
+    const uint64_t base = (uint64_t)p.start * (uint64_t)a.N;
+
+    uint32_t d[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int i = tile_row + r_loc + t;
+        bool real = i < p.rows;
+        int64_t src = (int64_t)p.start + i;
+        if (a.row_index) {
+            src = real ? a.row_index[src] : -1;
+            real = src >= 0 && src < a.x_rows;
+        }
+        const uint16_t *x = a.x + src * a.ldx + j0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) d[t][w] = 0;
+        if (real && j0 + 8 <= a.N) {
+            const v4u_t v = __builtin_nontemporal_load(reinterpret_cast<const v4u_t *>(x));
+#pragma unroll
+            for (int w = 0; w < 4; ++w) d[t][w] = v[w];
+        } else if (real) {
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (j0 + e < a.N) d[t][e >> 1] |= (uint32_t)x[e] << (16 * (e & 1));
+        }
+    }
+
+    // random bytes, as in quantize_kernel: with both directions stochastic and
+    // 16-element alignment a lane pair shares its Philox blocks
+    uint32_t rr[2][2], rc[2][2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        rr[t][0] = rr[t][1] = rc[t][0] = rc[t][1] = 0;
+        const uint64_t row = base + (uint64_t)(tile_row + r_loc + t) * (uint64_t)a.N;
+        if (ROW_SR && COL_SR && a.sr_pairs) {
+            const uint32_t odd = (uint32_t)(c & 1);
+            const DirOpts &o = odd ? a.col : a.row;
+            const uint64_t g = (o.index_base + row + (uint64_t)(col0 + 16 * (c >> 1))) >> 4;
+            uint32_t w0 = (uint32_t)g, w1 = (uint32_t)(g >> 32), w2 = o.tensor_id, w3 = odd;
+            philox10(w0, w1, w2, w3, o.key0, o.key1);
+            const auto other = [](uint32_t v) {
+                return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false);
+            };
+            const uint32_t x0 = other(odd ? w0 : w2), x1 = other(odd ? w1 : w3);
+            rr[t][0] = odd ? x0 : w0;
+            rr[t][1] = odd ? x1 : w1;
+            rc[t][0] = odd ? w2 : x0;
+            rc[t][1] = odd ? w3 : x1;
+        } else {
+            if (ROW_SR) rand8(a.row.index_base + row + (uint64_t)j0, a.row, 0u, rr[t][0], rr[t][1]);
+            if (COL_SR) rand8(a.col.index_base + row + (uint64_t)j0, a.col, 1u, rc[t][0], rc[t][1]);
+        }
+    }
+
+    uint32_t m[2][4], ramax[2], camax[4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m[t][w] = d[t][w] & 0x7FFF7FFFu;
+    {
+        const uint32_t r0 = pk_umax(pk_umax(m[0][0], m[0][1]), pk_umax(m[0][2], m[0][3]));
+        const uint32_t r1 = pk_umax(pk_umax(m[1][0], m[1][1]), pk_umax(m[1][2], m[1][3]));
+        uint32_t pk = pk_umax(__builtin_amdgcn_perm(r1, r0, 0x05040100u), __builtin_amdgcn_perm(r1, r0, 0x07060302u));
+        pk = lane_max<2, true>(lane_max<1, true>(pk));
+        ramax[0] = pk & 0xFFFFu;
+        ramax[1] = pk >> 16;
+        if (a.row.use_2d || a.col.use_2d) {
+            pk = max_over_rows(pk);
+            const uint32_t all = umax(pk & 0xFFFFu, pk >> 16);
+            if (a.row.use_2d) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) ramax[t] = tile_row + r_loc + t < p.rows ? all : 0u;
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                camax[w] = (j0 + 2 * w < a.N ? all : 0u) | (j0 + 2 * w + 1 < a.N ? all << 16 : 0u);
+        }
+        if (!a.col.use_2d) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) camax[w] = max_over_rows(pk_umax(m[0][w], m[1][w]));
+        }
+    }
+
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        bool nonfinite;
+        const uint32_t sc = scale_code_nf(ramax[t], nonfinite);
+        uint32_t packed;
+        if (ROW_SR) {
+            uint32_t even, odd;
+            sign_masks(d[t][0], d[t][1], d[t][2], d[t][3], even, odd);
+            packed = pack8_sr([&](int e) { return elem_hi(d[t][e >> 1], e & 1); }, sc,
+                              [&](int e) { return byte_to_b2(~rr[t][e >> 2], e & 3); }, even, odd, nonfinite);
+        } else {
+            packed = pack8_rne(d[t][0], d[t][1], d[t][2], d[t][3], sc, nonfinite);
+        }
+        *reinterpret_cast<uint32_t *>(&s_row[(r_loc + t) * 16 + 4 * c]) = packed;
+        if (c == 0) s_row_scale[r_loc + t] = (uint8_t)sc;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        const int w = u >> 1, h = u & 1;
+        bool nonfinite;
+        const uint32_t sc = scale_code_nf((camax[w] >> (16 * h)) & 0xFFFFu, nonfinite);
+        uint32_t packed = 0;   // rows 2 q (low nibble) and 2 q + 1
+        if (COL_SR) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t x = elem_hi(d[t][w], h);
+                uint32_t v = __float_as_uint(__builtin_ldexpf(__builtin_fabsf(__uint_as_float(x)), 1 - (int)sc));
+                v = v < (7u << 22) ? v : 7u << 22;
+                v = (v << 2) + byte_to_b2(~rc[t][u >> 2], u & 3);
+                packed |= ((v >> 24) | ((x >> 28) & 8u)) << (4 * t);
+            }
+        } else {
+            packed = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(0u, __builtin_bit_cast(bf16x2_t, pair_of(d[0][w], d[1][w], h)),
+                                                               scale_f32(sc), 0);
+        }
+        s_col[(8 * c + u) * 64 + 16 * wave + q] = nonfinite ? (uint8_t)0 : (uint8_t)packed;
+        if (q == 0) s_col_scale[(8 * c + u) * 4 + wave] = (uint8_t)sc;
+    }
+    __syncthreads();
+
+    // write out: threads 0..127 a row's slice each, 128..255 a column's
+    const int64_t n16 = cdiv(a.N, 16) * 16;
+    const bool col = threadIdx.x >= 128;
+    const int id = threadIdx.x & 127;
+    // blob row, block along the quantized axis, blocks of the padded axis, place of the group's part
+    const int64_t r = col ? col0 + (id & 15) + 16 * (id >> 6) : tile_row + id;
+    const int64_t blk = col ? tile_row / 32 + ((id >> 4) & 3) : blockIdx.x;
+    const int64_t nblk = (col ? padded(p.rows) : a.N_pad) / 32;
+    if (r >= (col ? n16 : (int64_t)units(p.rows, 16) * 16)) return;
+    uint8_t *qd = col ? a.q_col + (int64_t)p.k128 * n16 * 64 : a.q_row + (int64_t)p.r16 * 16 * (a.N_pad / 2);
+    uint8_t *sd = col ? a.s_col + (int64_t)p.k512 * n16 * 16 : a.s_row + (int64_t)p.r16 * 16 * (cdiv(a.N_pad, 512) * 16);
+    const int col_loc = (id & 15) + 16 * (id >> 6);
+    const uint8_t *src = col ? s_col + col_loc * 64 + 16 * ((id >> 4) & 3) : s_row + id * 16;
+    *reinterpret_cast<uint4 *>(qd + ((r / 16) * (nblk / 4) + blk / 4) * 1024 + (r % 16 + 16 * (blk % 4)) * 16) =
+        *reinterpret_cast<const uint4 *>(src);
+    const auto scale_at = [&](int64_t b) {
+        return sd + ((r / 16) * cdiv(nblk, 16) + b / 16) * 256 + 4 * (r % 16 + 16 * (b % 4)) + (b % 16) / 4;
+    };
+    *scale_at(blk) = col ? s_col_scale[col_loc * 4 + ((id >> 4) & 3)] : s_row_scale[id];
+    // the last four blocks along the axis also zero the scale bytes past them in the last scale atom
+    if (blk + 4 >= nblk)
+        for (int64_t b = blk + 4; b < cdiv(nblk, 16) * 16; b += 4) *scale_at(b) = 0;
+}
+
 template <bool DUAL, bool RHT>
 hipError_t launch_grouped(const QuantArgs &a, dim3 grid, hipStream_t stream) {
     constexpr int T = MX_LAYOUT_TILED;
@@ -1334,6 +1528,13 @@ hipError_t launch_quantize_grouped(const QuantArgs &a, bool dual, hipStream_t st
     const int64_t full = a.groups < a.M ? a.groups : a.M;
     QuantArgs b = a;
     const int64_t row_tiles = (a.M + (kTileRows - 1) * full) / kTileRows;
+    if (dual && !a.row.rht && !a.col.rht && row_tiles * cdiv(a.N, kTileCols) <= 2 * device_cu_count()) {
+        auto kernel = a.row.use_sr ? (a.col.use_sr ? quantize_narrow_kernel<true, true> : quantize_narrow_kernel<true, false>)
+                                   : (a.col.use_sr ? quantize_narrow_kernel<false, true>
+                                                   : quantize_narrow_kernel<false, false>);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(a.N_pad / 32), (unsigned)row_tiles), dim3(256), 0, stream, a);
+        return hipGetLastError();
+    }
     for (int64_t t0 = 0; t0 < row_tiles; t0 += kMaxRowTiles) {
         b.row_tile0 = t0;
         const dim3 grid((unsigned)cdiv(a.N, kTileCols),
