@@ -515,7 +515,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_grouped_stream_kernel(
         for (; k0 < c.kstream; k0 += C::kPeriod) period<C, false, 0, false, 0>(c, k0, acc, r, l);
         if constexpr (BIAS) add_bias<C>(acc, bias_bits);
         dma_part<C, 2, 2, 1, 0>(c, c.kstream + 2);
-        store_tile_private<C>(acc, 0, cur.tn, cur.rows, N, make_rsrc(Cout + cur.base, kBlob), ldc, wave, hidden(lane));
+        store_tile_private<C, !BIAS>(acc, 0, cur.tn, cur.rows, N, make_rsrc(Cout + cur.base, kBlob), ldc, wave, hidden(lane));
         if constexpr (BIAS) {
             asm volatile("" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
@@ -571,12 +571,14 @@ hipError_t launch_few(const GroupedGemmArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Whether the persistent form takes the product: bf16 output in whole 8-column
-// chunks and 32-bit offsets into both blobs and a tile of C.
+// Whether the persistent form takes the product: bf16 output, a bias whose rows
+// start at 16-byte boundaries, and 32-bit offsets into both blobs and a tile of
+// C.
 bool stream_fits(const GroupedGemmArgs &a, int64_t a_bytes, int64_t b_bytes) {
     constexpr int64_t kLimit = (int64_t(1) << 31) - 1;
     return a.out_dtype == MX_BF16 && a.groups <= kStreamGroups && a_bytes <= kLimit && b_bytes <= kLimit &&
-           256 * a.ldc * 2 <= kLimit && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
+           256 * a.ldc * 2 <= kLimit &&
+           (!a.bias || (a.N % 8 == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0));
 }
 
 hipError_t launch_stream(const GroupedGemmArgs &a, int cus, hipStream_t stream) {
@@ -643,7 +645,7 @@ hipError_t launch_gemm_grouped(const GroupedGemmArgs &a, hipStream_t stream) {
     if (a.M <= 32 * full || 10 * tiles(kFewM, kFewN) <= 26 * cus) return launch_few(a, stream);
     if (10 * tiles(128, 128) <= 13 * cus || a.M < 192 * full) return launch_shape<TailShape>(a, stream);
     const int64_t bytes = padded(a.K) / 2;
-    if (cus > 0 && a.N % 8 == 0 && a.K > 0 &&
+    if (cus > 0 && a.K > 0 &&
         stream_fits(a, (a.M + 15 * full) / 16 * 16 * bytes, a.groups * (cdiv(a.N, 16) * 16) * bytes))
         return launch_stream(a, cus, stream);
     return launch_shape<MainShape>(a, stream);
@@ -656,7 +658,7 @@ hipError_t launch_gemm_grouped_wgrad(const GroupedGemmArgs &a, hipStream_t strea
     const int cus = device_cu_count() / kXcds * kXcds;
     if (10 * a.groups * cdiv(a.N, 128) * cdiv(a.K, 128) <= 13 * cus) return launch_wgrad_shape<TailShape>(a, stream);
     const int64_t bytes = (a.M + 127 * full) / 128 * 64;   // a blob's per row
-    if (cus > 0 && a.K % 8 == 0 && stream_fits(a, cdiv(a.N, 16) * 16 * bytes, cdiv(a.K, 16) * 16 * bytes))
+    if (cus > 0 && stream_fits(a, cdiv(a.N, 16) * 16 * bytes, cdiv(a.K, 16) * 16 * bytes))
         return launch_wgrad_stream(a, cus, stream);
     return launch_wgrad_shape<MainShape>(a, stream);
 }

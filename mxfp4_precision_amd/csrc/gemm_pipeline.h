@@ -727,7 +727,10 @@ __host__ __device__ constexpr int epi_stores() {
     return C::kMA * 4;
 }
 
-template <class C>
+// PARTIAL: N need not be a multiple of 8.  The chunk that N ends in is then
+// written by elements, after its whole store was dropped (more stores than the
+// fixed count only make the next tile's first waits longer).
+template <class C, bool PARTIAL = false>
 __device__ __forceinline__ void store_tile_private(v16f (&acc)[C::kMB][C::kMA], int tm, int tn, int M, int N,
                                                    __amdgpu_buffer_rsrc_t rC, int ldc, int wave, int lane) {
     static_assert(C::kStages == 4, "the stream epilogue stages C through stage 3");
@@ -757,8 +760,20 @@ __device__ __forceinline__ void store_tile_private(v16f (&acc)[C::kMB][C::kMA], 
             const int r = 8 * s + (lane >> 3);
             const v4u_t v = *reinterpret_cast<const v4u_t *>(c_slot(r, lane & 7));
             const int row = row_w + 32 * p + r;
-            const uint32_t off = row < M && col < N ? (uint32_t)(row * ldc + col) * 2u : kOutOfRange;
+            const bool in = row < M && col < N, whole = !PARTIAL || col + 8 <= N;
+            const uint32_t at = (uint32_t)(row * ldc + col) * 2u, off = in && whole ? at : kOutOfRange;
             __builtin_amdgcn_raw_buffer_store_b128(v, rC, off, 0, kCachePolicyNT);
+            if constexpr (PARTIAL) {
+                const int first = tn * C::kBN + C::kWN * wn;   // the wave's columns
+                if (N % 8 != 0 && first < N && N < first + C::kWN) {
+#pragma unroll
+                    for (int e = 0; e < 7; ++e) {
+                        const short h = (short)(v[e >> 1] >> (16 * (e & 1)));
+                        const uint32_t at_e = in && !whole && col + e < N ? at + 2u * e : kOutOfRange;
+                        __builtin_amdgcn_raw_buffer_store_b16(h, rC, at_e, 0, 0);
+                    }
+                }
+            }
         }
     }
 }

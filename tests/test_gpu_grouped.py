@@ -105,6 +105,27 @@ def test_quantize_grouped_options(oracle_mod, row, col, N, base):
         check_blob(got[2 * d + 1], s, "scales %d" % d)
 
 
+@pytest.mark.parametrize("row,col,N", [(dict(), dict(), 2600), (dict(), dict(), 2595),
+                                       (dict(use_sr=True, seed=7, tensor_id=3), dict(use_sr=True, seed=7, tensor_id=3), 2608),
+                                       (dict(use_sr=True, seed=8), dict(use_sr=True, seed=9), 2600),
+                                       (dict(), dict(use_sr=True, seed=9), 2600), (dict(use_sr=True, seed=9), dict(), 2601),
+                                       (dict(use_2d=True), dict(use_2d=True), 2600), (dict(use_2d=True), dict(), 2600),
+                                       (dict(), dict(use_2d=True), 2601)])
+def test_quantize_grouped_of_many_tiles(oracle_mod, row, col, N):
+    """The same options where the 128 x 128 tiles outnumber the compute units."""
+    sizes = [0, 37, 700, 1, 64, 1500, 130, 800]
+    M = sum(sizes)
+    x = synth.random_bf16(N, (M, N), std=3.0)
+    x[40, :5] = [0x7F80, 0xFF80, 0x7FC0, 0x0001, 0x8000]
+    opt = lambda d: mx.quant_opts(use_2d_block=d.get("use_2d", False),  # noqa: E731
+                                  **{k: v for k, v in d.items() if k != "use_2d"})
+    got = quantize_grouped(x, ends_of(sizes), M, ro=opt(row), co=opt(col))
+    for d, o in ((0, row), (1, col)):
+        q, s = ref.grouped_blob(oracle_mod, x, ends_of(sizes), d, **o)
+        check_blob(got[2 * d], q, "data %d" % d)
+        check_blob(got[2 * d + 1], s, "scales %d" % d)
+
+
 @pytest.mark.parametrize("N,ldx", [(64, 64), (200, 264), (9, 16)])
 def test_quantize_grouped_gather(oracle_mod, N, ldx):
     x = synth.random_bf16(N, (50, N))
@@ -217,7 +238,8 @@ MANY = [(i * 29) % 97 if i % 6 else 0 for i in range(75)]          # ragged, som
 
 @pytest.mark.parametrize("sizes", [MANY, [700, 0, 256, 1, 513, 900, 31, 300], [3000]],
                          ids=lambda s: "%d_groups_%d_rows" % (len(s), sum(s)))
-@pytest.mark.parametrize("N,K,bias", [(1800, 40, False), (2056, 264, True), (1544, 776, False)])
+@pytest.mark.parametrize("N,K,bias", [(1800, 40, False), (2056, 264, True), (1544, 776, False), (1803, 130, False),
+                                         (1801, 72, True)])
 def test_product_of_many_tiles(oracle_mod, sizes, N, K, bias):
     """More output tiles than compute units: workgroups that run from tile to tile, across groups, over the rows in no
     group, with fewer k-steps than one k-group holds and with several."""
@@ -231,7 +253,7 @@ def test_product_of_many_tiles(oracle_mod, sizes, N, K, bias):
 
 @pytest.mark.parametrize("sizes", [MANY, [40, 0, 600, 129, 1300, 1, 0, 512] * 4],
                          ids=lambda s: "%d_groups_%d_rows" % (len(s), sum(s)))
-@pytest.mark.parametrize("N,K", [(300, 520), (600, 784)])
+@pytest.mark.parametrize("N,K", [(300, 520), (600, 784), (300, 525)])
 def test_wgrad_of_many_tiles(oracle_mod, sizes, N, K):
     """The same for the weights' gradient, where a tile's length is its group's."""
     if len(sizes) < 60:
