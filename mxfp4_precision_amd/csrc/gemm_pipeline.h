@@ -727,10 +727,12 @@ __host__ __device__ constexpr int epi_stores() {
     return C::kMA * 4;
 }
 
-// PARTIAL: N need not be a multiple of 8.  The chunk that N ends in is then
-// written by elements, after its whole store was dropped (more stores than the
-// fixed count only make the next tile's first waits longer).
-template <class C, bool PARTIAL = false>
+// ODD: N need not be a multiple of 8, nor rows of C start on 128-byte lines.
+// The chunk that N ends in is then written by elements, after its whole store
+// was dropped (more stores than the fixed count only make the next tile's
+// first waits longer), and no store is non-temporal, as neighbouring segments
+// share lines.
+template <class C, bool ODD = false>
 __device__ __forceinline__ void store_tile_private(v16f (&acc)[C::kMB][C::kMA], int tm, int tn, int M, int N,
                                                    __amdgpu_buffer_rsrc_t rC, int ldc, int wave, int lane) {
     static_assert(C::kStages == 4, "the stream epilogue stages C through stage 3");
@@ -760,14 +762,15 @@ __device__ __forceinline__ void store_tile_private(v16f (&acc)[C::kMB][C::kMA], 
             const int r = 8 * s + (lane >> 3);
             const v4u_t v = *reinterpret_cast<const v4u_t *>(c_slot(r, lane & 7));
             const int row = row_w + 32 * p + r;
-            const bool in = row < M && col < N, whole = !PARTIAL || col + 8 <= N;
+            const bool in = row < M && col < N, whole = !ODD || col + 8 <= N;
             const uint32_t at = (uint32_t)(row * ldc + col) * 2u, off = in && whole ? at : kOutOfRange;
-            __builtin_amdgcn_raw_buffer_store_b128(v, rC, off, 0, kCachePolicyNT);
-            if constexpr (PARTIAL) {
+            __builtin_amdgcn_raw_buffer_store_b128(v, rC, off, 0, ODD ? 0 : kCachePolicyNT);
+            if constexpr (ODD) {
                 const int first = tn * C::kBN + C::kWN * wn;   // the wave's columns
                 if (N % 8 != 0 && first < N && N < first + C::kWN) {
 #pragma unroll
                     for (int e = 0; e < 7; ++e) {
+                        if (e >= N % 8) break;
                         const short h = (short)(v[e >> 1] >> (16 * (e & 1)));
                         const uint32_t at_e = in && !whole && col + e < N ? at + 2u * e : kOutOfRange;
                         __builtin_amdgcn_raw_buffer_store_b16(h, rC, at_e, 0, 0);

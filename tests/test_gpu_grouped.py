@@ -3,6 +3,8 @@
 Blobs are compared byte for byte.  Products: the bars of the ungrouped GEMM, elementwise |C - bf16(C_ref)| <= 2
 ulp_bf16(max(|bf16(C_ref)|, tau)) with tau = (K_pad/32) 2^-24 sum_k |a_ik b_jk| (worst-case fp32 summation error of
 exact block sums), and for fp32 output |C - C_ref| <= tau elementwise."""
+import itertools
+
 import numpy as np
 import pytest
 
@@ -172,8 +174,7 @@ def run_product(oracle, x, w, ends, bias, what=""):
                 want[a:z] += b
                 S[a:z] += np.abs(b)
     tau = higham_tau(oracle_padded(K) + 32, S)
-    ldc = (N + 7) // 8 * 8 + 8
-    for dt, torch_dt in ((mx.MX_BF16, torch.int16), (mx.MX_F32, torch.float32)):
+    for (dt, torch_dt), ldc in itertools.product(((mx.MX_BF16, torch.int16), (mx.MX_F32, torch.float32)), strides(N)):
         C = torch.full((M, ldc), -1, dtype=torch_dt, device="cuda")
         mx.mx_gemm_a4w4_grouped(M, N, K, dev_i32(ends), e, *args, T, dt, bd, C, ldc)
         got = host(C)
@@ -185,6 +186,11 @@ def run_product(oracle, x, w, ends, bias, what=""):
     return want
 
 
+def strides(n):
+    """Row strides of C: with and without rows that start on 128-byte lines."""
+    return (n + 7) // 8 * 8 + 8, n // 64 * 64 + 128
+
+
 def oracle_padded(n):
     return -(-n // 128) * 128
 
@@ -193,7 +199,6 @@ def run_wgrad(oracle, dy, x, ends, what=""):
     (M, N), K, e = dy.shape, x.shape[1], len(ends)
     blobs = ref.grouped_blob(oracle, dy, ends, 1) + ref.grouped_blob(oracle, x, ends, 1)
     args = [dev_bytes(v) for v in blobs]
-    ldc = (K + 7) // 8 * 8 + 8
     want, S = np.zeros((e, N, K)), np.zeros((e, N, K))
     most = 0
     for i, (a, z) in enumerate(ref.spans(ends, M)):
@@ -202,7 +207,7 @@ def run_wgrad(oracle, dy, x, ends, what=""):
             want[i], S[i] = oracle.gemm_dense(qa[0], qa[1], qb[0], qb[1], N, K, z - a)
             most = max(most, oracle_padded(z - a))
     tau = higham_tau(most, S)
-    for dt, torch_dt in ((mx.MX_BF16, torch.int16), (mx.MX_F32, torch.float32)):
+    for (dt, torch_dt), ldc in itertools.product(((mx.MX_BF16, torch.int16), (mx.MX_F32, torch.float32)), strides(K)):
         C = torch.full((e, N + 1, ldc), -1, dtype=torch_dt, device="cuda")
         mx.mx_gemm_a4w4_grouped_wgrad(M, N, K, dev_i32(ends), e, *args, T, dt, C, ldc, (N + 1) * ldc)
         got = host(C)
