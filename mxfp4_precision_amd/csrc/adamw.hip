@@ -59,37 +59,36 @@ __device__ __forceinline__ void philox(uint32_t (&c)[4], uint32_t k0, uint32_t k
     }
 }
 
-// Eight elements at p + i, of which the first `left` exist (the others read
-// 0); FULL: all eight do.
-template <bool FULL, bool F32>
-__device__ __forceinline__ void load8(const void *p, int64_t i, int left, float (&v)[8]) {
+// A workgroup's chunk of an array, as a buffer: n elements of `size` bytes at
+// p, rounded up to whole dwords, which is what the range check of a load goes
+// by (p is 16-byte aligned, so they lie in the array's last 16-byte block).
+// Loads past the end read 0, without the branches that would make a tensor's
+// last chunk wait for one array after the other.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_of(const void *p, int64_t first, int n, int size) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(static_cast<const uint8_t *>(p)) + first * size, (short)0,
+                                             (n * size + 3) & ~3, 0x00020000);
+}
+constexpr int kNT = 2;   // cache policy: non-temporal
+
+// Elements i .. i + 7 of a chunk.
+template <bool F32>
+__device__ __forceinline__ void load8(__amdgpu_buffer_rsrc_t r, int i, float (&v)[8]) {
     if constexpr (F32) {
-        const float *s = static_cast<const float *>(p) + i;
-        if (FULL || left >= 8) {
-            const f4_t a = *reinterpret_cast<const f4_t *>(s);
-            const f4_t b = *(reinterpret_cast<const f4_t *>(s) + 1);
+        const f4_t a = __builtin_bit_cast(f4_t, __builtin_amdgcn_raw_buffer_load_b128(r, i * 4, 0, 0));
+        const f4_t b = __builtin_bit_cast(f4_t, __builtin_amdgcn_raw_buffer_load_b128(r, i * 4 + 16, 0, 0));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = e < left ? s[e] : 0.0f;
-        }
+        for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
     } else {
-        const uint16_t *s = static_cast<const uint16_t *>(p) + i;
-        if (FULL || left >= 8) {
-            const u4_t a = __builtin_nontemporal_load(reinterpret_cast<const u4_t *>(s));
+        const u4_t a = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(r, i * 2, 0, kNT));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[2 * e] = __uint_as_float(a[e] << 16);
-                v[2 * e + 1] = __uint_as_float(a[e] & 0xFFFF0000u);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = e < left ? __uint_as_float((uint32_t)s[e] << 16) : 0.0f;
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(a[e] << 16);
+            v[2 * e + 1] = __uint_as_float(a[e] & 0xFFFF0000u);
         }
     }
 }
 
+// The first `left` of eight elements to p + i; FULL: all eight.
 template <bool FULL, bool F32>
 __device__ __forceinline__ void store8(void *p, int64_t i, int left, const float (&v)[8]) {
     if constexpr (F32) {
@@ -115,23 +114,6 @@ __device__ __forceinline__ void store8(void *p, int64_t i, int left, const float
             for (int e = 0; e < 8; ++e)
                 if (e < left) s[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
         }
-    }
-}
-
-// Eight E4M3 codes at p + i (a multiple of 8) and their block's scale byte.
-template <bool FULL>
-__device__ __forceinline__ void load_codes(const uint8_t *p, const uint8_t *scale, int64_t i, int left, u2_t &w,
-                                           uint32_t &c) {
-    w = u2_t{0u, 0u};
-    c = 0;
-    if (!FULL && left <= 0) return;
-    c = scale[i / 32];
-    if (FULL || left >= 8) {
-        w = __builtin_nontemporal_load(reinterpret_cast<const u2_t *>(p + i));
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < left) w[e >> 2] |= (uint32_t)p[i + e] << (8 * (e & 3));
     }
 }
 
@@ -243,26 +225,45 @@ __device__ __forceinline__ void sqrt8(const float (&v)[8], float (&root)[8]) {
     }
 }
 
-// This lane's eight elements from i on, of which `left` exist.
+// This lane's eight elements of the chunk from `first` on (n elements; FULL:
+// kChunk of them).
 template <bool FULL, bool P32, bool G32, bool S8, bool SR>
-__device__ __forceinline__ void update8(const AdamwBatch &b, const AdamwItem &it, const mx_adamw_step &h, int64_t i,
-                                        int left) {
+__device__ __forceinline__ void update8(const AdamwBatch &b, const AdamwItem &it, const mx_adamw_step &h, int64_t first,
+                                        int n) {
 #pragma clang fp contract(off)
+    const int local = threadIdx.x * kLaneElems, left = FULL ? 8 : (n - local < 0 ? 0 : (n - local > 8 ? 8 : n - local));
+    const int64_t i = first + local;
     float p[8], g[8], m[8], v[8];
-    load8<FULL, G32>(it.grad, i, left, g);
-    load8<FULL, P32>(it.param, i, left, p);
+    load8<G32>(chunk_of(it.grad, first, n, G32 ? 4 : 2), local, g);
+    load8<P32>(chunk_of(it.param, first, n, P32 ? 4 : 2), local, p);
     if constexpr (S8) {
-        u2_t wm, wv;
-        uint32_t cm, cv;
-        load_codes<FULL>(static_cast<const uint8_t *>(it.m), it.ms, i, left, wm, cm);
-        load_codes<FULL>(static_cast<const uint8_t *>(it.v), it.vs, i, left, wv, cv);
+        u2_t wm = __builtin_bit_cast(u2_t, __builtin_amdgcn_raw_buffer_load_b64(chunk_of(it.m, first, n, 1), local, 0, kNT));
+        u2_t wv = __builtin_bit_cast(u2_t, __builtin_amdgcn_raw_buffer_load_b64(chunk_of(it.v, first, n, 1), local, 0, kNT));
+        uint32_t cm = 0, cv = 0;
+        if (FULL || left > 0) {
+            cm = it.ms[i / 32];
+            cv = it.vs[i / 32];
+        }
+        if constexpr (!FULL) {   // a dword that the end cuts holds other bytes too
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int keep = left - 4 * e;
+                const uint32_t mask = keep >= 4 ? ~0u : (keep <= 0 ? 0u : (1u << (8 * keep)) - 1u);
+                wm[e] &= mask;
+                wv[e] &= mask;
+            }
+        }
         decode8(wm, cm, m);
         decode8(wv, cv, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = v[e] * v[e];
     } else {
-        load8<FULL, true>(it.m, i, left, m);
-        load8<FULL, true>(it.v, i, left, v);
+        load8<true>(chunk_of(it.m, first, n, 4), local, m);
+        load8<true>(chunk_of(it.v, first, n, 4), local, v);
+    }
+    if constexpr (!FULL && !G32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = e < left ? g[e] : 0.0f;
     }
     float root[8];
 #pragma unroll
@@ -327,13 +328,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwBatch b) {
     const int64_t first = (int64_t)(blockIdx.x - (t ? b.t[t - 1].chunk_end : 0u)) * kChunk;
     mx_adamw_step h = b.step;
     if (b.dev_step) h = *b.dev_step;
-    const int64_t i = first + (int64_t)threadIdx.x * kLaneElems;
-    if (first + kChunk <= it.numel) {
-        update8<true, P32, G32, S8, SR>(b, it, h, i, 8);
-    } else {
-        const int64_t l = it.numel - i;
-        update8<false, P32, G32, S8, SR>(b, it, h, i, l < 0 ? 0 : (l > 8 ? 8 : (int)l));
-    }
+    if (first + kChunk <= it.numel) update8<true, P32, G32, S8, SR>(b, it, h, first, kChunk);
+    else update8<false, P32, G32, S8, SR>(b, it, h, first, (int)(it.numel - first));
 }
 
 template <bool P32, bool G32>
