@@ -15,15 +15,6 @@ namespace {
 
 typedef int v4i_t __attribute__((ext_vector_type(4)));
 
-// Tile `b` of `total` in XCD-contiguous order, or -1 (a workgroup past its
-// XCD's share).
-__device__ __forceinline__ int xcd_position(int b, int total) {
-    const int xcd = b % kXcds, local = b / kXcds;
-    const int per = total / kXcds, rem = total % kXcds;
-    if (local >= per + (xcd < rem ? 1 : 0)) return -1;
-    return xcd * per + (xcd < rem ? xcd : rem) + local;
-}
-
 // One output tile per workgroup.  Rows of C in no group are written as 0.
 template <class C, bool OUT_BF16, bool BIAS>
 __global__ __launch_bounds__(C::kThreads) void gemm_grouped_kernel(const int32_t *__restrict__ ends, int groups, int M,

@@ -19,7 +19,6 @@ typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u_t __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u_t __attribute__((ext_vector_type(2)));
 
-constexpr int kXcds = 8;
 // Offset that lies past every operand buffer: a buffer load there returns 0.
 constexpr uint32_t kOutOfRange = 0x80000000u;
 // buffer-store cache policy: non-temporal (C is not read again by the kernel)

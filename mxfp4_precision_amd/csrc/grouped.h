@@ -34,6 +34,15 @@ __device__ __forceinline__ int wave_scan(int v) {
     return v;
 }
 
+// Number `b` of `total` in XCD-contiguous order, or -1 (a workgroup past its
+// XCD's share).
+__device__ __forceinline__ int xcd_position(int b, int total) {
+    const int xcd = b % kXcds, local = b / kXcds;
+    const int per = total / kXcds, rem = total % kXcds;
+    if (local >= per + (xcd < rem ? 1 : 0)) return -1;
+    return xcd * per + (xcd < rem ? xcd : rem) + local;
+}
+
 // Where a group lies, in rows and in blob units.
 struct GroupPos {
     int group;       // its index, or `groups` for the rows behind the last group

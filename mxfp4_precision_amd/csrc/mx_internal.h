@@ -42,6 +42,8 @@ struct QuantArgs {
     int64_t x_rows;
 };
 
+constexpr int kXcds = 8;   // dies of the chip, each with an L2 of its own; workgroups go to them round-robin
+
 struct GroupedGemmArgs {
     const int32_t *ends;        // cumulative row ends of the groups, device memory
     int groups;

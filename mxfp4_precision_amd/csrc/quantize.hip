@@ -1203,7 +1203,8 @@ hipError_t launch_quantize_fp6(const QuantArgs &a, bool dual, mx_layout layout, 
 
 // Grouped rows, row-wise blob only, nearest even, blocks of 32: what serving
 // needs, in a kernel short enough that its latency is three dependent loads
-// (ends, index, row).  A wave takes 16 rows x 512 columns: 4 data atoms and
+// (ends, index, row): 8 rows of 2048 take 4.7 us, where quantize_kernel takes
+// 6.6; 65536 gathered rows of 4096 98 us (138).  A wave takes 16 rows x 512 columns: 4 data atoms and
 // one scale atom.  Lane L reads 8 elements of rows 4 t + L / 16 (256
 // consecutive bytes of a row per 16 lanes), a block is a quad of lanes, and a
 // 4 x 4 transpose inside the quad gives lane L the whole block L % 16 / 4 of
@@ -1223,53 +1224,28 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int lane) {
     exchange(w[1], w[3], lane & 2, by2);
 }
 
-constexpr int kEarlyIndex = 256;
-
-__global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a, uint32_t chunks) {
-    const int lane = threadIdx.x & 63;
-    const uint32_t id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int unit = (int)(id / chunks), chunk = (int)(id % chunks);
-    int start = 0, rows = 0, before = 0;   // the unit's group, and the units before it
-    // a short index is read along with the ends instead of after them
-    __shared__ int32_t s_index[4][kEarlyIndex];
-    const bool early = a.row_index && a.M <= kEarlyIndex;
-    if (early) {
-#pragma unroll
-        for (int i = 0; i < kEarlyIndex; i += 64)
-            if (i + lane < a.M) s_index[threadIdx.x >> 6][i + lane] = a.row_index[i + lane];
-    }
-    {
-        GroupCarry c;
-        bool found = false;
-        for (int base = 0; base < a.groups; base += 64) {
-            const GroupLane g = group_block<16, false>(a.ends, a.groups, (int)a.M, base, lane, c);
-            const uint64_t past = __builtin_amdgcn_ballot_w64(unit < g.tiles);
-            if (past) {
-                const int l = __builtin_ctzll(past);
-                start = __builtin_amdgcn_readlane(g.start, l);
-                rows = __builtin_amdgcn_readlane(g.rows, l);
-                before = __builtin_amdgcn_readlane(g.tiles, l) - units(rows, 16);
-                found = true;
-                break;
-            }
-        }
-        if (!found) return;
-    }
-    const int row0 = (unit - before) * 16;
-    const int64_t col0 = (int64_t)chunk * 512 + 8 * (lane & 15);
-    v4u_t d[4][4];   // [atom][t]
-    const uint16_t *src[4];
+// Rows row0 + 4 t + lane / 16 of a group that starts at `start`: where they lie
+// in x, or null.  index: a copy of the row index, or null.
+__device__ __forceinline__ void unit_rows(const QuantArgs &a, int start, int rows, int row0, int lane,
+                                          const int32_t *index, const uint16_t *(&src)[4]) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         const int r = row0 + 4 * t + (lane >> 4);
         int64_t at = (int64_t)start + r;
         bool real = r < rows;
         if (a.row_index) {
-            at = real ? (early ? s_index[threadIdx.x >> 6][at] : a.row_index[at]) : -1;
+            at = real ? (index ? index[at] : a.row_index[at]) : -1;
             real = at >= 0 && at < a.x_rows;
         }
         src[t] = real ? a.x + at * a.ldx : nullptr;
     }
+}
+
+// Columns 512 chunk .. + 511 of the 16 rows src, the blob's row group `unit`.
+__device__ __forceinline__ void quantize_unit(const QuantArgs &a, const uint16_t *const (&src)[4], int unit, int chunk,
+                                              int lane) {
+    const int64_t col0 = (int64_t)chunk * 512 + 8 * (lane & 15);
+    v4u_t d[4][4];   // [atom][t]
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
@@ -1317,6 +1293,78 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a, uint32_
     }
     const uint32_t s01 = lane & 1 ? scales[1] : scales[0], s23 = lane & 1 ? scales[3] : scales[2];
     *reinterpret_cast<uint32_t *>(a.s_row + ((int64_t)unit * kgroups + chunk) * 256 + slot * 4) = lane & 2 ? s23 : s01;
+}
+
+constexpr int kEarlyIndex = 256;
+
+// Wave `id` of the launch: unit id / chunks, chunk id % chunks.
+__global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a, uint32_t chunks) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int unit = (int)(id / chunks), chunk = (int)(id % chunks);
+    int start = 0, rows = 0, before = 0;   // the unit's group, and the units before it
+    // a short index is read along with the ends instead of after them
+    __shared__ int32_t s_index[4][kEarlyIndex];
+    const bool early = a.row_index && a.M <= kEarlyIndex;
+    if (early) {
+#pragma unroll
+        for (int i = 0; i < kEarlyIndex; i += 64)
+            if (i + lane < a.M) s_index[threadIdx.x >> 6][i + lane] = a.row_index[i + lane];
+    }
+    {
+        GroupCarry c;
+        bool found = false;
+        for (int base = 0; base < a.groups; base += 64) {
+            const GroupLane g = group_block<16, false>(a.ends, a.groups, (int)a.M, base, lane, c);
+            const uint64_t past = __builtin_amdgcn_ballot_w64(unit < g.tiles);
+            if (past) {
+                const int l = __builtin_ctzll(past);
+                start = __builtin_amdgcn_readlane(g.start, l);
+                rows = __builtin_amdgcn_readlane(g.rows, l);
+                before = __builtin_amdgcn_readlane(g.tiles, l) - units(rows, 16);
+                found = true;
+                break;
+            }
+        }
+        if (!found) return;
+    }
+    const uint16_t *src[4];
+    unit_rows(a, start, rows, (unit - before) * 16, lane, early ? s_index[threadIdx.x >> 6] : nullptr, src);
+    quantize_unit(a, src, unit, chunk, lane);
+}
+
+// The same for long gathered inputs, in an order that keeps the rows of a token
+// that several groups hold (sorted by token within each) close in time: slice
+// s of 2^shift takes units [u s >> shift, u (s + 1) >> shift) of every group of u
+// units, and an XCD runs a contiguous range of slices, so that all but the
+// first read of a row finds it in that XCD's L2.  Workgroup = unit; its waves
+// take the chunks in turn.  At most 64 groups, one a lane.  16384 rows of 4096,
+// each in 4 of 64 groups: 97.7 -> 73.7 us (the same rows all in L2: 50; slices
+// of 8, 4, 2, 0.25 and 0.06 MB: 83.3, 77.1, 73.7, 73.2 and 75.1).
+__global__ __launch_bounds__(256) void quantize_slices_kernel(QuantArgs a, int chunks, int shift) {
+    const int lane = threadIdx.x & 63;
+    GroupCarry c;
+    const GroupLane g = group_block<16, false>(a.ends, a.groups, (int)a.M, 0, lane, c);
+    const int k = xcd_position(blockIdx.x, c.tiles);
+    if (k < 0) return;
+    const int u = units(g.rows, 16);
+    const auto before = [&](int s) {   // units before slice s, of all groups
+        return __builtin_amdgcn_readlane(wave_scan<false>((int)(((uint32_t)u * (uint32_t)s) >> shift)), 63);
+    };
+    int s = 0;
+    for (int bit = (1 << shift) >> 1; bit > 0; bit >>= 1)
+        if (before(s + bit) <= k) s += bit;
+    const int first = (int)(((uint32_t)u * (uint32_t)s) >> shift);
+    const int n = (int)(((uint32_t)u * (uint32_t)(s + 1)) >> shift) - first;
+    const int sum = wave_scan<false>(n), left = k - before(s);
+    const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(left < sum));
+    const int in_group = __builtin_amdgcn_readlane(first - (sum - n), l) + left;
+    const int unit = __builtin_amdgcn_readlane(g.tiles - u, l) + in_group;
+    const uint16_t *src[4];
+    unit_rows(a, __builtin_amdgcn_readlane(g.start, l), __builtin_amdgcn_readlane(g.rows, l), in_group * 16, lane, nullptr,
+              src);
+    for (int chunk = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); chunk < chunks; chunk += 4)
+        quantize_unit(a, src, unit, chunk, lane);
 }
 
 // Workgroups of a quantize_rows_kernel launch.
@@ -1519,6 +1567,16 @@ hipError_t launch_grouped(const QuantArgs &a, dim3 grid, hipStream_t stream) {
 // Grid rows: the most 128-row tiles that M rows in a.groups groups can need;
 // workgroups past those that there are return at once.
 hipError_t launch_quantize_grouped(const QuantArgs &a, bool dual, hipStream_t stream) {
+    if (!dual && !a.row.use_sr && !a.row.use_2d && !a.row.rht && a.row_index && a.groups <= 64 &&
+        a.M >= 256 * (int64_t)a.groups && a.M < (int64_t(1) << 22) && a.x_rows * a.N * 2 >= (int64_t(16) << 20)) {
+        // slices of about 2 MB of x
+        int shift = 3;
+        while (shift < 9 && (a.x_rows * a.N * 2 >> shift) > (int64_t(2) << 20)) ++shift;
+        const int64_t units = (a.M + 15 * (a.groups < a.M ? a.groups : a.M)) / 16;
+        hipLaunchKernelGGL(quantize_slices_kernel, dim3((unsigned)(cdiv(units, kXcds) * kXcds)), dim3(256), 0, stream, a,
+                           (int)cdiv(a.N_pad, 512), shift);
+        return hipGetLastError();
+    }
     // (a grid holds fewer than 2^32 threads)
     if (!dual && !a.row.use_sr && !a.row.use_2d && !a.row.rht && quantize_rows_blocks(a) < int64_t(1) << 24) {
         hipLaunchKernelGGL(quantize_rows_kernel, dim3((unsigned)quantize_rows_blocks(a)), dim3(256), 0, stream, a,

@@ -142,6 +142,25 @@ def test_quantize_grouped_gather(oracle_mod, N, ldx):
         check_blob(got[2 * d + 1], s, "scales %d" % d)
 
 
+@pytest.mark.parametrize("N,groups", [(2048, 7), (2051, 7), (520, 64)])
+@pytest.mark.parametrize("order", ["sorted", "any"])
+def test_quantize_grouped_gathers_many_rows(oracle_mod, N, groups, order):
+    """Row-wise blobs of long gathered inputs, groups of very unequal size among them."""
+    rng = np.random.default_rng(N + groups)
+    rows = (16 << 20) // (2 * N) + 100
+    x = synth.random_bf16(N, (rows, N))
+    sizes = [0, 1500, 3, 2000, 701, 1, 1200] if groups == 7 else [int(v) for v in rng.integers(0, 640, groups - 1)] + [900]
+    M = sum(sizes) + 3
+    index = rng.integers(-1, rows + 1, M)
+    if order == "sorted":
+        for a, z in ref.spans(ends_of(sizes), M):
+            index[a:z].sort()
+    got = quantize_grouped(x, ends_of(sizes), M, index=index, dual=False)
+    q, s = ref.grouped_blob(oracle_mod, ref.gathered(x, index, M), ends_of(sizes), 0)
+    check_blob(got[0], q, "data")
+    check_blob(got[1], s, "scales")
+
+
 @pytest.mark.parametrize("ends", [[-5, 20, 10, 400, 300], [500] * 3, [2 ** 31 - 1, -2 ** 31, 7], [40, 0, 40]])
 def test_ends_are_clamped(oracle_mod, ends):
     """Ends that no router should give lead to the clamped groups, in every operator."""
