@@ -450,7 +450,8 @@ mx_status mx_adamw_step_values(const mx_adamw_opts *opts, mx_adamw_step *step);
  * One step over tensors[0..count) (a host array, read before the call
  * returns).  Tensors with numel == 0 are skipped; no two tensors may overlap.
  * One launch for up to 48 tensors.
- * Requires param, grad, states and param_copy 16-byte aligned.
+ * Requires param, grad, states and param_copy 16-byte aligned; the bytes of
+ * their last 4-byte word past numel are read (never written or used).
  * Errors: MX_ERR_INVALID_ARGUMENT (NULL, count < 0, numel < 0, betas outside
  * [0, 1), eps < 0, step < 1, use_sr not 0 or 1, non-finite values),
  * MX_ERR_MISALIGNED, MX_ERR_UNSUPPORTED (a dtype, numel above 2^33, a bf16

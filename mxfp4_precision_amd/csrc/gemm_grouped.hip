@@ -13,8 +13,6 @@
 namespace mx {
 namespace {
 
-typedef int v4i_t __attribute__((ext_vector_type(4)));
-
 // One output tile per workgroup.  Rows of C in no group are written as 0.
 template <class C, bool OUT_BF16, bool BIAS>
 __global__ __launch_bounds__(C::kThreads) void gemm_grouped_kernel(const int32_t *__restrict__ ends, int groups, int M,
@@ -303,9 +301,11 @@ __global__ __launch_bounds__(C::kThreads) void gemm_grouped_wgrad_kernel(const i
 // An XCD's workgroups walk a contiguous range of the tile order round-robin,
 // so that they share A rows and B columns in its L2.  The ranges hold equally
 // many tiles, or, with WGRAD, equally much work: a tile costs its k-steps and
-// about kTileCost more for its stores.
+// kTileCost more for its stores.  Training steps of 16384 rows in 16 groups and
+// 65536 in 32, same box: 409 and 1253 us (kTileCost 8: 419 and 1259, 0: 406 and
+// 1264, equally many tiles: 5% more).
 constexpr int kStreamGroups = 512;   // groups that the table holds
-constexpr int kTileCost = 8;
+constexpr int kTileCost = 4;
 
 struct StreamTile {
     int ksteps;      // 0: zeros
@@ -619,7 +619,7 @@ hipError_t launch_wgrad_shape(const GroupedGemmArgs &a, hipStream_t stream) {
 constexpr int64_t kMaxBlocks = int64_t(1) << 22;
 
 bool grouped_gemm_fits(int64_t M, int64_t N, int groups) {
-    return max_tiles(M, groups, 64) * cdiv(N, 32) < kMaxBlocks;
+    return max_tiles(M, groups, 128) * cdiv(N, 128) < kMaxBlocks;
 }
 
 bool grouped_wgrad_fits(int64_t N, int64_t K, int groups) {
@@ -645,7 +645,8 @@ hipError_t launch_gemm_grouped(const GroupedGemmArgs &a, hipStream_t stream) {
     const int64_t full = a.groups < a.M ? a.groups : a.M;
     const int cus = device_cu_count() / kXcds * kXcds;
     const auto tiles = [&](int bm, int bn) { return (a.M + bm * full / 2) / bm * cdiv(a.N, bn); };
-    if (a.M <= 32 * full || 10 * tiles(kFewM, kFewN) <= 26 * cus) return launch_few(a, stream);
+    const bool few_fits = max_tiles(a.M, a.groups, kFewM) * cdiv(a.N, kFewN) < 2 * kMaxBlocks;   // of 256 threads
+    if (few_fits && (a.M <= 32 * full || 10 * tiles(kFewM, kFewN) <= 26 * cus)) return launch_few(a, stream);
     if (10 * tiles(128, 128) <= 13 * cus || a.M < 192 * full) return launch_shape<TailShape>(a, stream);
     const int64_t bytes = padded(a.K) / 2;
     if (cus > 0 && a.K > 0 &&

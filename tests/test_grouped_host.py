@@ -1,6 +1,9 @@
 """Host-side checks of the grouped operators and of AdamW: sizes, refusals before any launch, step values, and the
 tests' own references against the definitions."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -109,6 +112,8 @@ def test_grouped_gemm_refusals(binding):
     assert call(M=1 << 20, K=1 << 13) == UNSUPPORTED          # 2^20 rows of 4 KB: 4 GiB
     assert call(N=1 << 20, K=1 << 13, ldc=1 << 20) == UNSUPPORTED
     assert call(M=1 << 25, N=1 << 15, K=64, ldc=1 << 15) == UNSUPPORTED   # tiles
+    assert call(M=1 << 21, N=1 << 14, K=64, ldc=1 << 14) == mx.MX_ERR_DEVICE_UNSUPPORTED
+    assert call(M=1 << 20, N=1 << 14, K=64, ldc=1 << 14, groups=1 << 14) == mx.MX_ERR_DEVICE_UNSUPPORTED
     assert call(K=0, A=0, As=0, B=0, Bs=0) == mx.MX_ERR_DEVICE_UNSUPPORTED
     assert call(M=0) == mx.MX_SUCCESS and call(N=0) == mx.MX_SUCCESS
 
@@ -131,6 +136,14 @@ def test_grouped_wgrad_refusals(binding):
     assert call(M=1 << 29, N=64, K=64, ldc=64, stride=4096) == UNSUPPORTED
     assert call(M=0, A=0, As=0, B=0, Bs=0) == mx.MX_ERR_DEVICE_UNSUPPORTED     # all groups empty: zeros
     assert call(N=0, stride=0) == mx.MX_SUCCESS and call(K=0) == mx.MX_SUCCESS
+
+
+def test_import_loads_no_hip_runtime():
+    """Importing the package must leave the choice of the HIP runtime to torch: two of them in a process do not work."""
+    code = "import mxfp4_precision_amd as mx; assert mx._marshal; print('amdhip' in open('/proc/self/maps').read())"
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert out.stdout.strip() == "False", out.stdout + out.stderr
 
 
 def test_argument_conversions(binding):
