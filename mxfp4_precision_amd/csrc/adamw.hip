@@ -32,6 +32,9 @@
 //    decode (ldexp and a NaN select per value), the encode (codes masked and
 //    shifted one by one) and the square root took 434 us.
 
+#include <cstddef>
+#include <cstring>
+
 #include "mx_internal.h"
 
 namespace mx {
@@ -227,8 +230,8 @@ __device__ __forceinline__ void sqrt8(const float (&v)[8], float (&root)[8]) {
 
 // This lane's eight elements of the chunk from `first` on (n elements; FULL:
 // kChunk of them).
-template <bool FULL, bool P32, bool G32, bool S8, bool SR>
-__device__ __forceinline__ void update8(const AdamwBatch &b, const AdamwItem &it, const mx_adamw_step &h, int64_t first,
+template <bool FULL, bool P32, bool G32, bool S8, bool SR, typename TABLE>
+__device__ __forceinline__ void update8(const TABLE &b, const AdamwItem &it, const mx_adamw_step &h, int64_t first,
                                         int n) {
 #pragma clang fp contract(off)
     const int local = threadIdx.x * kLaneElems, left = FULL ? 8 : (n - local < 0 ? 0 : (n - local > 8 ? 8 : n - local));
@@ -311,8 +314,8 @@ __device__ __forceinline__ void update8(const AdamwBatch &b, const AdamwItem &it
     }
 }
 
-template <bool P32, bool G32, bool S8, bool SR>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwBatch b) {
+template <bool P32, bool G32, bool S8, bool SR, int ITEMS>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwTable<ITEMS> b) {
     // the tensor of this workgroup's chunk
     int t = 0;
     {
@@ -332,12 +335,22 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwBatch b) {
     else update8<false, P32, G32, S8, SR>(b, it, h, first, (int)(it.numel - first));
 }
 
-template <bool P32, bool G32>
-hipError_t launch_states(const AdamwBatch &b, bool s8, bool sr, unsigned blocks, hipStream_t stream) {
-    auto kernel = !s8 ? adamw_kernel<P32, G32, false, false>
-                      : (sr ? adamw_kernel<P32, G32, true, true> : adamw_kernel<P32, G32, true, false>);
+template <bool P32, bool G32, int ITEMS>
+hipError_t launch_table(const AdamwTable<ITEMS> &b, bool s8, bool sr, unsigned blocks, hipStream_t stream) {
+    auto kernel = !s8 ? adamw_kernel<P32, G32, false, false, ITEMS>
+                      : (sr ? adamw_kernel<P32, G32, true, true, ITEMS> : adamw_kernel<P32, G32, true, false, ITEMS>);
     hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kThreads), 0, stream, b);
     return hipGetLastError();
+}
+
+constexpr int kFewItems = 6;
+
+template <bool P32, bool G32>
+hipError_t launch_states(const AdamwBatch &b, bool s8, bool sr, unsigned blocks, hipStream_t stream) {
+    if (b.count > kFewItems) return launch_table<P32, G32>(b, s8, sr, blocks, stream);
+    AdamwTable<kFewItems> few;
+    memcpy(&few, &b, offsetof(AdamwBatch, t) + b.count * sizeof(AdamwItem));
+    return launch_table<P32, G32>(few, s8, sr, blocks, stream);
 }
 
 }  // namespace

@@ -635,7 +635,8 @@ mx_status mx_adamw(const mx_adamw_tensor *tensors, int64_t count, const mx_adamw
         if (t.param_copy && opts->param_dtype != MX_F32)
             return fail(MX_ERR_UNSUPPORTED, "tensor %lld: a bf16 copy needs fp32 parameters", (long long)i);
     }
-    mx::AdamwBatch b{};
+    mx::AdamwBatch b;   // entries past its count are never read
+    b.count = 0;
     b.beta1 = (float)opts->beta1;
     b.one_minus_beta1 = (float)(1.0 - opts->beta1);
     b.beta2 = (float)opts->beta2;

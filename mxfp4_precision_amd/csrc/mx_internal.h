@@ -67,13 +67,17 @@ struct AdamwItem {
     uint32_t tensor_id;
 };
 constexpr int kAdamwItems = 48;
-struct AdamwBatch {
-    AdamwItem t[kAdamwItems];
+// One launch's kernel arguments.  They are copied for each launch, so a few
+// tensors go with a short table.
+template <int ITEMS>
+struct AdamwTable {
     int count;
     float beta1, one_minus_beta1, beta2, one_minus_beta2, eps;
     mx_adamw_step step;
     const mx_adamw_step *dev_step;
+    AdamwItem t[ITEMS];
 };
+using AdamwBatch = AdamwTable<kAdamwItems>;
 static_assert(sizeof(AdamwBatch) <= 4000, "kernel arguments");
 
 // Grid dimension y of one launch holds at most 65536 workgroups on gfx950

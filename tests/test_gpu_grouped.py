@@ -442,3 +442,12 @@ def test_blobs_past_4_gib():
     want = v.reshape(N // 16, K // 128, 4, 16, 16).sum(dim=(1, 2, 4)).reshape(N)
     # sums of multiples of 1/2 below 2^23: exact
     assert torch.equal(C.double(), want.expand(rows, N))
+
+
+def test_wgrad_without_rows():
+    """No rows at all: every expert's gradient is written as 0, without operands."""
+    groups, N, K = 9, 1032, 2056
+    C = torch.full((groups, N, K), -1, dtype=torch.int16, device="cuda")
+    mx.mx_gemm_a4w4_grouped_wgrad(0, N, K, dev_i32([0] * groups), groups, None, None, None, None, T, mx.MX_BF16, C, K,
+                                  N * K)
+    assert not host(C).any()
