@@ -27,7 +27,7 @@
 //    moves 4.8 TB/s).  Plain fp32 loads, as the lines are written again at
 //    once: 418 us with non-temporal ones.
 //  - MXFP8 states, bf16 parameters and gradients, stochastic (10.1 bytes), 201M
-//    elements: 381 us, 5.3 TB/s, memory and arithmetic about even (65 vector
+//    elements: 385 us, 5.3 TB/s, memory and arithmetic about even (65 vector
 //    instructions an element, 13 of them Philox).  The earlier forms of the
 //    decode (ldexp and a NaN select per value), the encode (codes masked and
 //    shifted one by one) and the square root took 434 us.
@@ -239,6 +239,18 @@ __device__ __forceinline__ void update8(const TABLE &b, const AdamwItem &it, con
     float p[8], g[8], m[8], v[8];
     load8<G32>(chunk_of(it.grad, first, n, G32 ? 4 : 2), local, g);
     load8<P32>(chunk_of(it.param, first, n, P32 ? 4 : 2), local, p);
+    uint32_t bits[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    // the random words while the loads are in flight
+    const auto draw = [&]() {
+        const uint64_t k = (uint64_t)i >> 2;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t c[4] = {(uint32_t)(k + q), (uint32_t)((k + q) >> 32), it.tensor_id, 4u};
+            philox(c, (uint32_t)h.seed, (uint32_t)(h.seed >> 32));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bits[4 * q + e] = c[e];
+        }
+    };
     if constexpr (S8) {
         u2_t wm = __builtin_bit_cast(u2_t, __builtin_amdgcn_raw_buffer_load_b64(chunk_of(it.m, first, n, 1), local, 0, kNT));
         u2_t wv = __builtin_bit_cast(u2_t, __builtin_amdgcn_raw_buffer_load_b64(chunk_of(it.v, first, n, 1), local, 0, kNT));
@@ -247,6 +259,7 @@ __device__ __forceinline__ void update8(const TABLE &b, const AdamwItem &it, con
             cm = it.ms[i / 32];
             cv = it.vs[i / 32];
         }
+        if constexpr (SR) draw();
         if constexpr (!FULL) {   // a dword that the end cuts holds other bytes too
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -291,17 +304,6 @@ __device__ __forceinline__ void update8(const TABLE &b, const AdamwItem &it, con
             av = max_u(av, __float_as_uint(root[e]));
         }
         const uint32_t cm = scale_of(block_max(am)), cv = scale_of(block_max(av));
-        uint32_t bits[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-        if constexpr (SR) {
-            const uint64_t n = (uint64_t)i >> 2;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t c[4] = {(uint32_t)(n + q), (uint32_t)((n + q) >> 32), it.tensor_id, 4u};
-                philox(c, (uint32_t)h.seed, (uint32_t)(h.seed >> 32));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) bits[4 * q + e] = c[e];
-            }
-        }
         store_codes<FULL>(static_cast<uint8_t *>(it.m), i, left, encode8<SR, false>(m, cm, bits));
         store_codes<FULL>(static_cast<uint8_t *>(it.v), i, left, encode8<SR, true>(root, cv, bits));
         if ((FULL || left > 0) && (threadIdx.x & 3) == 0) {

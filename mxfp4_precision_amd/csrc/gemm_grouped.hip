@@ -302,7 +302,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_grouped_wgrad_kernel(const i
 // so that they share A rows and B columns in its L2.  The ranges hold equally
 // many tiles, or, with WGRAD, equally much work: a tile costs its k-steps and
 // kTileCost more for its stores.  Training steps of 16384 rows in 16 groups and
-// 65536 in 32, same box: 409 and 1253 us (kTileCost 8: 419 and 1259, 0: 406 and
+// 65536 in 32, run in turn: 409 and 1253 us (kTileCost 8: 419 and 1259, 0: 406 and
 // 1264, equally many tiles: 5% more).
 constexpr int kStreamGroups = 512;   // groups that the table holds
 constexpr int kTileCost = 4;
@@ -573,7 +573,7 @@ bool stream_fits(const GroupedGemmArgs &a, int64_t a_bytes, int64_t b_bytes) {
            (!a.bias || (a.N % 8 == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0));
 }
 
-// The epilogue for any N and row stride (ODD).  Same box, the other epilogue in
+// The epilogue for any N and row stride (ODD).  Run in turn, the other epilogue in
 // parentheses: 20510 rows of 809 columns, stride 816, K 1204 in 7 groups 42.7 us
 // with its quantization (46.9 non-temporal); a training step of 16384 rows,
 // 4096 x 2048 in 16 groups 441 us (480 without non-temporal stores).

@@ -420,7 +420,7 @@ def test_side_stream_and_graph_replays(oracle_mod):
 
 def test_blobs_past_4_gib():
     """Weights of many experts whose blobs pass 32-bit offsets: the last group's product is right."""
-    groups, N, K = 40, 8192, 30720
+    groups, N, K = 40, 8192, 32768
     each = N * K // 2
     assert groups * each > 1 << 32
     B = torch.zeros(groups * each, dtype=torch.uint8, device="cuda")
