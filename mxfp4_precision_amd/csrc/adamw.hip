@@ -345,6 +345,7 @@ hipError_t launch_table(const AdamwTable<ITEMS> &b, bool s8, bool sr, unsigned b
     return hipGetLastError();
 }
 
+// Tensors of a short table: three small tensors 4.7 us a step (5.2 with the long one).
 constexpr int kFewItems = 6;
 
 template <bool P32, bool G32>

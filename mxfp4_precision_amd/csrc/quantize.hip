@@ -1567,8 +1567,13 @@ hipError_t launch_grouped(const QuantArgs &a, dim3 grid, hipStream_t stream) {
 // Grid rows: the most 128-row tiles that M rows in a.groups groups can need;
 // workgroups past those that there are return at once.
 hipError_t launch_quantize_grouped(const QuantArgs &a, bool dual, hipStream_t stream) {
-    if (!dual && !a.row.use_sr && !a.row.use_2d && !a.row.rht && a.row_index && a.groups <= 64 &&
-        a.M >= 256 * (int64_t)a.groups && a.M < (int64_t(1) << 22) && a.x_rows * a.N * 2 >= (int64_t(16) << 20)) {
+    const bool plain_rows = !dual && !a.row.use_sr && !a.row.use_2d && !a.row.rht;
+    // More gathered rows than x has: some are read again.  In us, by units in
+    // order / in slices: 512 rows of 1024 into 2 of 8 groups 6.1 / 5.7, 2048 of
+    // 2048 into 4 of 64 10.4 / 9.4, 16384 of 2048 into 2 of 16 27.1 / 22.7; into 1
+    // of 64 (8192 of 4096) 17.0 / 19.0.
+    if (plain_rows && a.row_index && a.groups <= 64 && a.M > a.x_rows && a.M > kEarlyIndex && a.N_pad > 512 &&
+        a.M < (int64_t(1) << 22)) {
         // slices of about 2 MB of x
         int shift = 3;
         while (shift < 9 && (a.x_rows * a.N * 2 >> shift) > (int64_t(2) << 20)) ++shift;
@@ -1578,7 +1583,7 @@ hipError_t launch_quantize_grouped(const QuantArgs &a, bool dual, hipStream_t st
         return hipGetLastError();
     }
     // (a grid holds fewer than 2^32 threads)
-    if (!dual && !a.row.use_sr && !a.row.use_2d && !a.row.rht && quantize_rows_blocks(a) < int64_t(1) << 24) {
+    if (plain_rows && quantize_rows_blocks(a) < int64_t(1) << 24) {
         hipLaunchKernelGGL(quantize_rows_kernel, dim3((unsigned)quantize_rows_blocks(a)), dim3(256), 0, stream, a,
                            (uint32_t)cdiv(a.N_pad, 512));
         return hipGetLastError();
@@ -1586,6 +1591,10 @@ hipError_t launch_quantize_grouped(const QuantArgs &a, bool dual, hipStream_t st
     const int64_t full = a.groups < a.M ? a.groups : a.M;
     QuantArgs b = a;
     const int64_t row_tiles = (a.M + (kTileRows - 1) * full) / kTileRows;
+    // In us, 128 x 128 tiles / narrow ones, full groups: 64 tiles 6.1 / 4.2 (SR 8.0
+    // / 5.1), 256 tiles 6.3 / 7.1 (8.5 / 8.9), 512 tiles 8.4 / 10.5; but the count
+    // bounds ragged groups from above, and a training step of 558 rows in 32
+    // groups, 1472 x 1216, (432 tiles by the bound) runs 105 / 98.
     if (dual && !a.row.rht && !a.col.rht && row_tiles * cdiv(a.N, kTileCols) <= 2 * device_cu_count()) {
         auto kernel = a.row.use_sr ? (a.col.use_sr ? quantize_narrow_kernel<true, true> : quantize_narrow_kernel<true, false>)
                                    : (a.col.use_sr ? quantize_narrow_kernel<false, true>

@@ -142,12 +142,14 @@ def test_quantize_grouped_gather(oracle_mod, N, ldx):
         check_blob(got[2 * d + 1], s, "scales %d" % d)
 
 
-@pytest.mark.parametrize("N,groups", [(2048, 7), (2051, 7), (520, 64)])
+@pytest.mark.parametrize("N,groups", [(2048, 7), (2051, 7), (520, 64), (200, 64)])
 @pytest.mark.parametrize("order", ["sorted", "any"])
-def test_quantize_grouped_gathers_many_rows(oracle_mod, N, groups, order):
-    """Row-wise blobs of long gathered inputs, groups of very unequal size among them."""
+@pytest.mark.parametrize("rows", [90, 4000, 30000])
+def test_quantize_grouped_gathers_many_rows(oracle_mod, N, groups, order, rows):
+    """Row-wise blobs of long gathered inputs, groups of very unequal size among them, rows read many times and
+    mostly not at all."""
     rng = np.random.default_rng(N + groups)
-    rows = (16 << 20) // (2 * N) + 100
+    rows = min(rows, (1 << 24) // N)
     x = synth.random_bf16(N, (rows, N))
     sizes = [0, 1500, 3, 2000, 701, 1, 1200] if groups == 7 else [int(v) for v in rng.integers(0, 640, groups - 1)] + [900]
     M = sum(sizes) + 3
