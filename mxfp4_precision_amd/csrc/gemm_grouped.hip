@@ -91,7 +91,9 @@ __global__ __launch_bounds__(C::kThreads) void gemm_grouped_kernel(const int32_t
 // MA atoms) x 32 columns; its four waves take k-step 4 h + wave of every
 // k-group h, so each reads one byte of the scale dwords that all four load,
 // and their sums are added in wave order through LDS.  Up to eight k-groups
-// are in flight per wave.
+// are in flight per wave.  192 rows in 32 groups, N 1536, K 4096: 17 us, 6.2 TB/s
+// of weights (128x128 tiles 19); two or four k-groups in flight, 16 or 64
+// columns and non-temporal loads are no faster.
 constexpr int kFewM = 64, kFewNB = 2, kFewN = 16 * kFewNB;
 
 template <int MA, int DEPTH>
