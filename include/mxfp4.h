@@ -453,7 +453,9 @@ mx_status mx_adamw_step_values(const mx_adamw_opts *opts, mx_adamw_step *step);
  * Requires param, grad, states and param_copy 16-byte aligned; the bytes of
  * their last 4-byte word past numel are read (never written or used).
  * Errors: MX_ERR_INVALID_ARGUMENT (NULL, count < 0, numel < 0, betas outside
- * [0, 1), eps < 0, step < 1, use_sr not 0 or 1, non-finite values),
+ * [0, 1), eps < 0, step < 1, use_sr not 0 or 1, lr, weight_decay, grad_scale,
+ * eps or a step value that is not finite in fp32; values in device_step are
+ * used as they are),
  * MX_ERR_MISALIGNED, MX_ERR_UNSUPPORTED (a dtype, numel above 2^33, a bf16
  * copy of bf16 parameters), MX_ERR_DEVICE_UNSUPPORTED, MX_ERR_HIP.
  */

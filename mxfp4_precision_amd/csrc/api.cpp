@@ -572,17 +572,6 @@ mx_status mx_gemm_a4w4_grouped_wgrad(int64_t M, int64_t N, int64_t K, const int3
 
 namespace {
 
-mx_status check_adamw_opts(const mx_adamw_opts *o) {
-    if (!o) return fail(MX_ERR_INVALID_ARGUMENT, "opts is NULL");
-    if (!std::isfinite(o->lr) || !std::isfinite(o->weight_decay) || !std::isfinite(o->eps))
-        return fail(MX_ERR_INVALID_ARGUMENT, "lr, weight_decay and eps must be finite");
-    if (!(o->beta1 >= 0 && o->beta1 < 1) || !(o->beta2 >= 0 && o->beta2 < 1))
-        return fail(MX_ERR_INVALID_ARGUMENT, "beta1=%g and beta2=%g must be in [0, 1)", o->beta1, o->beta2);
-    if (o->eps < 0) return fail(MX_ERR_INVALID_ARGUMENT, "eps=%g must be >= 0", o->eps);
-    if (o->step < 1) return fail(MX_ERR_INVALID_ARGUMENT, "step=%lld must be >= 1", (long long)o->step);
-    return MX_SUCCESS;
-}
-
 mx_adamw_step step_of(const mx_adamw_opts &o) {
     mx_adamw_step s;
     s.grad_scale = (float)o.grad_scale;
@@ -591,6 +580,25 @@ mx_adamw_step step_of(const mx_adamw_opts &o) {
     s.root_factor = (float)(1.0 / std::sqrt(1.0 - std::pow(o.beta2, (double)o.step)));
     s.seed = o.seed;
     return s;
+}
+
+mx_status check_adamw_opts(const mx_adamw_opts *o) {
+    if (!o) return fail(MX_ERR_INVALID_ARGUMENT, "opts is NULL");
+    if (!std::isfinite(o->lr) || !std::isfinite(o->weight_decay) || !std::isfinite(o->eps))
+        return fail(MX_ERR_INVALID_ARGUMENT, "lr, weight_decay and eps must be finite");
+    if (!(o->beta1 >= 0 && o->beta1 < 1) || !(o->beta2 >= 0 && o->beta2 < 1))
+        return fail(MX_ERR_INVALID_ARGUMENT, "beta1=%g and beta2=%g must be in [0, 1)", o->beta1, o->beta2);
+    if (o->eps < 0) return fail(MX_ERR_INVALID_ARGUMENT, "eps=%g must be >= 0", o->eps);
+    if (o->step < 1) return fail(MX_ERR_INVALID_ARGUMENT, "step=%lld must be >= 1", (long long)o->step);
+    // (finite doubles can be too large for the fp32 values that the kernel computes with)
+    const mx_adamw_step s = step_of(*o);
+    if (!std::isfinite(s.grad_scale) || !std::isfinite(s.decay) || !std::isfinite(s.step_size) ||
+        !std::isfinite(s.root_factor) || !std::isfinite((float)o->eps))
+        return fail(MX_ERR_INVALID_ARGUMENT,
+                    "grad_scale=%g, decay=%g, step_size=%g, root_factor=%g and eps=%g must be finite in fp32",
+                    (double)s.grad_scale, (double)s.decay, (double)s.step_size, (double)s.root_factor,
+                    (double)(float)o->eps);
+    return MX_SUCCESS;
 }
 
 bool float_dtype(int t) { return t == MX_F32 || t == MX_BF16; }
