@@ -552,8 +552,8 @@ mx_status mx_gemm_a4w4_grouped_wgrad(int64_t M, int64_t N, int64_t K, const int3
     const char *name = "mx_gemm_a4w4_grouped_wgrad";
     MX_TRY(check_grouped_gemm(name, M, N, K, group_ends, groups, A, A_scale, B, B_scale, layout, out_dtype, C, ldc, K,
                               M > 0));
-    // (a stride too large for the product cannot be an allocated tensor)
-    if (groups > 1 && (ldc >= (int64_t(1) << 40) || group_stride < N * ldc))
+    // group_stride < N * ldc, in a form that cannot overflow
+    if (groups > 1 && (group_stride < 0 || group_stride / ldc < N))
         return fail(MX_ERR_INVALID_ARGUMENT, "group_stride=%lld must be >= N * ldc", (long long)group_stride);
     if (group_stride % 8) return fail(MX_ERR_MISALIGNED, "group_stride=%lld must be a multiple of 8", (long long)group_stride);
     // a group's part holds at most padded(M) rows

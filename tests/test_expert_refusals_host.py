@@ -39,3 +39,25 @@ def test_adamw_refuses_values_that_are_not_finite_in_fp32(bad):
     for grad_scale, want in ((3.4028234663852886e38, mx.MX_ERR_DEVICE_UNSUPPORTED), (3.4028236e38, INVALID)):
         opts = mx.adamw_opts(lr=1e-3, step=1, grad_scale=grad_scale)
         assert status(mx.mx_adamw, table, 1, opts, 0) == want
+
+
+@pytest.fixture(params=["extension", "ctypes"])
+def binding(request, monkeypatch):
+    """Both conversions of the grouped calls' arguments."""
+    if request.param == "ctypes":
+        monkeypatch.setattr(mx, "_marshal", None)
+
+
+def wgrad(**kw):
+    a = dict(M=0, N=16, K=40, ends=A16, groups=2, A=0, As=0, B=0, Bs=0, layout=mx.MX_LAYOUT_TILED, dt=mx.MX_BF16, C=A16,
+             ldc=40, stride=640)
+    a.update(kw)
+    return status(mx.mx_gemm_a4w4_grouped_wgrad, *a.values(), 0)
+
+
+@pytest.mark.parametrize("N,ldc,stride", [(1 << 29, 1 << 35, 0), (1 << 29, 1 << 35, 1 << 40), (1 << 28, 5 << 36, 1 << 62),
+                                          (1 << 25, (1 << 38) + 8, 1 << 28), (16, 1 << 40, 1 << 43)])
+def test_wgrad_strides_past_64_bits(binding, N, ldc, stride):
+    """N * ldc passes 64 bits: no group stride reaches it, whatever the product's low bits are."""
+    assert N * ldc > stride
+    assert wgrad(N=N, K=8, ldc=ldc, stride=stride) == INVALID
