@@ -625,7 +625,8 @@ bool grouped_gemm_fits(int64_t M, int64_t N, int groups) {
 }
 
 bool grouped_wgrad_fits(int64_t N, int64_t K, int groups) {
-    return groups * (cdiv(N, 128) * cdiv(K, 128)) < kMaxBlocks;
+    const int64_t tiles = cdiv(N, 128) * cdiv(K, 128);
+    return tiles < kMaxBlocks && groups * tiles < kMaxBlocks;   // (the product alone can pass 64 bits)
 }
 
 // Which form takes a product, by the tiles that M rows spread evenly over the

@@ -61,3 +61,12 @@ def test_wgrad_strides_past_64_bits(binding, N, ldc, stride):
     """N * ldc passes 64 bits: no group stride reaches it, whatever the product's low bits are."""
     assert N * ldc > stride
     assert wgrad(N=N, K=8, ldc=ldc, stride=stride) == INVALID
+
+
+@pytest.mark.parametrize("N,K,groups", [(1 << 29, 1 << 29, 1 << 20), (1 << 28, 1 << 28, 1 << 22),
+                                        ((1 << 29) + 128, 1 << 29, 1 << 20), (1 << 15, 1 << 14, 1 << 9)])
+def test_wgrad_tiles_past_64_bits(binding, N, K, groups):
+    """Output tiles whose number passes 64 bits are too many, whatever its low bits are."""
+    assert wgrad(N=N, K=K, groups=groups, ldc=K, stride=N * K) == mx.MX_ERR_UNSUPPORTED
+    assert wgrad(N=1 << 14, K=1 << 14, groups=1 << 8, ldc=1 << 14, stride=1 << 28) == mx.MX_ERR_UNSUPPORTED
+    assert wgrad(N=1 << 14, K=1 << 14, groups=(1 << 8) - 1, ldc=1 << 14, stride=1 << 28) == mx.MX_ERR_DEVICE_UNSUPPORTED
