@@ -26,7 +26,7 @@ decltype(&mx_gemm_a4w4_grouped) g_gemm_grouped;
 decltype(&mx_gemm_a4w4_grouped_wgrad) g_gemm_grouped_wgrad;
 PyObject *g_dptr, *g_i32ptr, *g_stream;   // the Python binding's converters
 PyObject *g_int32;                        // torch.int32, once torch is imported
-PyObject *s_is_cuda, *s_data_ptr, *s_dtype, *s_is_contiguous, *s_numel, *s_cuda_stream, *s_torch;
+PyObject *s_is_cuda, *s_data_ptr, *s_dtype, *s_is_contiguous, *s_numel, *s_torch;
 
 // Arguments of one call in order; after a failed conversion (`bad`, Python
 // error set) the others return 0.
@@ -132,12 +132,11 @@ struct Args {
         }
         return (const T *)b.buf;
     }
+    // a handle; the Python converter takes the rest (None, streams)
     hipStream_t stream() {
         PyObject *o = next();
         if (bad) return nullptr;
-        if (PyLong_CheckExact(o)) return (hipStream_t)PyLong_AsVoidPtr(o);
-        if (o != Py_None) return (hipStream_t)address(PyObject_GetAttr(o, s_cuda_stream));
-        return (hipStream_t)address(PyObject_CallOneArg(g_stream, o));
+        return (hipStream_t)address(PyLong_CheckExact(o) ? Py_NewRef(o) : PyObject_CallOneArg(g_stream, o));
     }
 };
 
@@ -249,6 +248,5 @@ PyMODINIT_FUNC PyInit__marshal(void) {
     s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
     s_numel = PyUnicode_InternFromString("numel");
     s_torch = PyUnicode_InternFromString("torch");
-    s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
     return PyModule_Create(&g_module);
 }

@@ -70,3 +70,35 @@ def test_wgrad_tiles_past_64_bits(binding, N, K, groups):
     assert wgrad(N=N, K=K, groups=groups, ldc=K, stride=N * K) == mx.MX_ERR_UNSUPPORTED
     assert wgrad(N=1 << 14, K=1 << 14, groups=1 << 8, ldc=1 << 14, stride=1 << 28) == mx.MX_ERR_UNSUPPORTED
     assert wgrad(N=1 << 14, K=1 << 14, groups=(1 << 8) - 1, ldc=1 << 14, stride=1 << 28) == mx.MX_ERR_DEVICE_UNSUPPORTED
+
+
+def quantize(**kw):
+    a = dict(x=A16, x_rows=9, N=16, ldx=16, index=None, M=9, ends=A16, groups=2, ro=None, co=None,
+             layout=mx.MX_LAYOUT_TILED, q=A16, s=A16, qc=A16, sc=A16, stream=0)
+    a.update(kw)
+    return status(mx.mx_quantize_grouped, *a.values())
+
+
+class Handle(int):
+    """An integer handle of another type."""
+
+
+class Stream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+@pytest.mark.parametrize("handle", [7, 0, (1 << 64) - 8, Handle(7), True], ids=repr)
+def test_stream_handles(binding, handle):
+    assert quantize(stream=handle) == mx.MX_ERR_DEVICE_UNSUPPORTED
+    assert quantize(stream=Stream(handle)) == mx.MX_ERR_DEVICE_UNSUPPORTED
+
+
+@pytest.mark.parametrize("stream", [1 << 64, 1 << 70, -(1 << 70)], ids=repr)
+def test_a_stream_that_is_no_address_is_refused(binding, stream):
+    """Refused before the call is made, not after it has gone to another stream."""
+    try:
+        got = quantize(stream=stream)
+    except OverflowError:
+        return
+    assert got == mx.MX_ERR_DEVICE_UNSUPPORTED      # ctypes takes an address modulo 2^64
