@@ -159,7 +159,7 @@ def lib() -> ctypes.CDLL:
     if _marshal is not None:
         address = lambda f: ctypes.cast(f, vp).value  # noqa: E731
         _marshal.bind(address(L.mx_quantize_grouped), address(L.mx_gemm_a4w4_grouped),
-                      address(L.mx_gemm_a4w4_grouped_wgrad), _dptr, _i32ptr, _stream)
+                      address(L.mx_gemm_a4w4_grouped_wgrad), _dptr, _i32ptr, _stream, mx_quant_opts)
     _lib = L
     return L
 

@@ -25,6 +25,7 @@ decltype(&mx_quantize_grouped) g_quantize_grouped;
 decltype(&mx_gemm_a4w4_grouped) g_gemm_grouped;
 decltype(&mx_gemm_a4w4_grouped_wgrad) g_gemm_grouped_wgrad;
 PyObject *g_dptr, *g_i32ptr, *g_stream;   // the Python binding's converters
+PyObject *g_quant_opts;                   // ... and its options structure
 PyObject *g_int32;                        // torch.int32, once torch is imported
 PyObject *s_is_cuda, *s_data_ptr, *s_dtype, *s_is_contiguous, *s_numel, *s_torch;
 
@@ -116,21 +117,17 @@ struct Args {
         }
         return (int)r;
     }
-    // a ctypes structure of the given size, or None
-    template <typename T>
-    const T *structure() {
+    // an mx_quant_opts of the Python binding, or None
+    const mx_quant_opts *options() {
         PyObject *o = next();
         if (bad || o == Py_None) return nullptr;
-        if (PyObject_GetBuffer(o, &views[held], PyBUF_SIMPLE) != 0) {
+        const int is = PyObject_IsInstance(o, g_quant_opts);
+        if (is == 0) PyErr_Format(PyExc_TypeError, "mx_quant_opts or None is required, got %R", (PyObject *)Py_TYPE(o));
+        if (is <= 0 || PyObject_GetBuffer(o, &views[held], PyBUF_SIMPLE) != 0) {
             bad = true;
             return nullptr;
         }
-        const Py_buffer &b = views[held++];
-        if (b.len != (Py_ssize_t)sizeof(T)) {
-            PyErr_SetString(PyExc_TypeError, "an options structure of another type");
-            bad = true;
-        }
-        return (const T *)b.buf;
+        return (const mx_quant_opts *)views[held++].buf;
     }
     // a handle; the Python converter takes the rest (None, streams)
     hipStream_t stream() {
@@ -168,7 +165,7 @@ PyObject *quantize_grouped(PyObject *, PyObject *const *v, Py_ssize_t n) {
     const int64_t groups = a.i64(7);
     const int32_t *ends = a.i32ptr(groups);
     const int g = a.i32();
-    const mx_quant_opts *ro = a.structure<mx_quant_opts>(), *co = a.structure<mx_quant_opts>();
+    const mx_quant_opts *ro = a.options(), *co = a.options();
     const int layout = a.i32();
     void *q = a.ptr(), *s = a.ptr(), *qc = a.ptr(), *sc = a.ptr();
     const hipStream_t st = a.stream();
@@ -215,17 +212,19 @@ PyObject *gemm_grouped_wgrad(PyObject *, PyObject *const *v, Py_ssize_t n) {
 
 PyObject *bind(PyObject *, PyObject *args) {
     unsigned long long q, g, w;
-    PyObject *dptr, *i32ptr, *stream;
-    if (!PyArg_ParseTuple(args, "KKKOOO", &q, &g, &w, &dptr, &i32ptr, &stream)) return nullptr;
+    PyObject *dptr, *i32ptr, *stream, *opts;
+    if (!PyArg_ParseTuple(args, "KKKOOOO", &q, &g, &w, &dptr, &i32ptr, &stream, &opts)) return nullptr;
     g_quantize_grouped = (decltype(g_quantize_grouped))(uintptr_t)q;
     g_gemm_grouped = (decltype(g_gemm_grouped))(uintptr_t)g;
     g_gemm_grouped_wgrad = (decltype(g_gemm_grouped_wgrad))(uintptr_t)w;
     Py_INCREF(dptr);
     Py_INCREF(i32ptr);
     Py_INCREF(stream);
+    Py_INCREF(opts);
     g_dptr = dptr;
     g_i32ptr = i32ptr;
     g_stream = stream;
+    g_quant_opts = opts;
     Py_RETURN_NONE;
 }
 

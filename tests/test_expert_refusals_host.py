@@ -1,5 +1,7 @@
 """Refusals of the grouped calls and of AdamW whose arguments reach the limits of their types: on the CPU, before any
 launch."""
+import ctypes
+
 import pytest
 
 import mxfp4_precision_amd as mx
@@ -102,3 +104,18 @@ def test_a_stream_that_is_no_address_is_refused(binding, stream):
     except OverflowError:
         return
     assert got == mx.MX_ERR_DEVICE_UNSUPPORTED      # ctypes takes an address modulo 2^64
+
+
+class Options(mx.mx_quant_opts):
+    """A caller's own kind of options."""
+
+
+@pytest.mark.parametrize("bad", [bytes, bytearray, lambda n: (ctypes.c_uint8 * n)(), lambda n: mx.mx_adamw_step()],
+                         ids=["bytes", "bytearray", "array", "structure"])
+@pytest.mark.parametrize("which", ["ro", "co"])
+def test_only_options_are_taken_as_options(binding, bad, which):
+    """Other objects are refused, also where they hold as many bytes."""
+    for good in (None, mx.quant_opts(use_sr=True), Options()):
+        assert quantize(**{which: good}) == mx.MX_ERR_DEVICE_UNSUPPORTED
+    with pytest.raises((TypeError, ctypes.ArgumentError)):
+        quantize(**{which: bad(ctypes.sizeof(mx.mx_quant_opts))})
