@@ -10,6 +10,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include "grouped_forms.h"
 #include "mx_internal.h"
 
 namespace {

@@ -9,6 +9,7 @@
 
 #include "gemm_pipeline.h"
 #include "grouped.h"
+#include "grouped_forms.h"
 
 namespace mx {
 namespace {
@@ -94,8 +95,6 @@ __global__ __launch_bounds__(C::kThreads) void gemm_grouped_kernel(const int32_t
 // are in flight per wave.  192 rows in 32 groups, N 1536, K 4096: 17 us, 6.2 TB/s
 // of weights (128x128 tiles 19); two or four k-groups in flight, 16 or 64
 // columns and non-temporal loads are no faster.
-constexpr int kFewM = 64, kFewNB = 2, kFewN = 16 * kFewNB;
-
 template <int MA, int DEPTH>
 __device__ __forceinline__ void few_rows_sum(__amdgpu_buffer_rsrc_t rA, __amdgpu_buffer_rsrc_t rAs,
                                              __amdgpu_buffer_rsrc_t rB, __amdgpu_buffer_rsrc_t rBs, int gA0, int nGA,
@@ -306,7 +305,6 @@ __global__ __launch_bounds__(C::kThreads) void gemm_grouped_wgrad_kernel(const i
 // kTileCost more for its stores.  Training steps of 16384 rows in 16 groups and
 // 65536 in 32, run in turn: 409 and 1253 us (kTileCost 8: 419 and 1259, 0: 406 and
 // 1264, equally many tiles: 5% more).
-constexpr int kStreamGroups = 512;   // groups that the table holds
 constexpr int kTileCost = 4;
 
 struct StreamTile {
@@ -534,13 +532,6 @@ __global__ __launch_bounds__(C::kThreads) void gemm_grouped_stream_kernel(
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-// Most tiles of `tile` rows that M rows in `groups` groups and the rows
-// behind the last group can need.
-int64_t max_tiles(int64_t M, int groups, int tile) {
-    const int64_t g = (groups < M ? groups : M) + 1;
-    return (M + (tile - 1) * g) / tile;
-}
-
 template <class S>
 hipError_t launch_shape(const GroupedGemmArgs &a, hipStream_t stream) {
     using C = Cfg<Fp4Fmt, S>;
@@ -565,22 +556,10 @@ hipError_t launch_few(const GroupedGemmArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Whether the persistent form takes the product: bf16 output, a bias whose rows
-// start at 16-byte boundaries, and 32-bit offsets into both blobs and a tile of
-// C.
-bool stream_fits(const GroupedGemmArgs &a, int64_t a_bytes, int64_t b_bytes) {
-    constexpr int64_t kLimit = (int64_t(1) << 31) - 1;
-    return a.out_dtype == MX_BF16 && a.groups <= kStreamGroups && a_bytes <= kLimit && b_bytes <= kLimit &&
-           256 * a.ldc * 2 <= kLimit &&
-           (!a.bias || (a.N % 8 == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0));
-}
-
 // The epilogue for any N and row stride (ODD).  Run in turn, the other epilogue in
 // parentheses: 20510 rows of 809 columns, stride 816, K 1204 in 7 groups 42.7 us
 // with its quantization (46.9 non-temporal); a training step of 16384 rows,
 // 4096 x 2048 in 16 groups 441 us (480 without non-temporal stores).
-bool odd_rows(const GroupedGemmArgs &a, int64_t columns) { return columns % 8 != 0 || a.ldc % 64 != 0; }
-
 hipError_t launch_stream(const GroupedGemmArgs &a, int cus, hipStream_t stream) {
     using C = Cfg<Fp4Fmt, MainShape>;
     auto kernel = odd_rows(a, a.N) ? (a.bias ? gemm_grouped_stream_kernel<C, false, true, true>
@@ -595,7 +574,7 @@ hipError_t launch_stream(const GroupedGemmArgs &a, int cus, hipStream_t stream) 
 
 hipError_t launch_wgrad_stream(const GroupedGemmArgs &a, int cus, hipStream_t stream) {
     using C = Cfg<Fp4Fmt, MainShape>;
-    auto kernel = odd_rows(a, a.K) || a.group_stride % 64 != 0 ? gemm_grouped_stream_kernel<C, true, false, true>
+    auto kernel = wgrad_odd_rows(a) ? gemm_grouped_stream_kernel<C, true, false, true>
                                                                : gemm_grouped_stream_kernel<C, true, false, false>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)cus), dim3(C::kThreads), 0, stream, a.ends, a.groups, (int)a.M, (int)a.N,
                        (int)a.K, 0, 0, (int)cdiv(a.K, C::kBN), a.A, a.As, a.B, a.Bs, a.bias,
@@ -616,58 +595,24 @@ hipError_t launch_wgrad_shape(const GroupedGemmArgs &a, hipStream_t stream) {
 
 }  // namespace
 
-// Workgroups of the largest grid the entry points let through (a grid of
-// 512-thread workgroups must stay below 2^32 threads).
-constexpr int64_t kMaxBlocks = int64_t(1) << 22;
-
-bool grouped_gemm_fits(int64_t M, int64_t N, int groups) {
-    return max_tiles(M, groups, 128) * cdiv(N, 128) < kMaxBlocks;
-}
-
-bool grouped_wgrad_fits(int64_t N, int64_t K, int groups) {
-    const int64_t tiles = cdiv(N, 128) * cdiv(K, 128);
-    return tiles < kMaxBlocks && groups * tiles < kMaxBlocks;   // (the product alone can pass 64 bits)
-}
-
-// Which form takes a product, by the tiles that M rows spread evenly over the
-// groups with rows make (the real spread is known on the device only).
-// Measured on MI355X in us, few rows / 128x128 / persistent 256x256:
-//   64 groups of 4, N 2048, K 4096    52 /  75 /  78
-//   64 groups of 32                   68 /  77 /  79
-//   64 groups of 64                   93 /  81 /  80
-//   4 groups of 256, N 1200, K 1024  5.5 / 6.5 / 9.9
-//   12 groups of 64                  5.2 / 6.0 / 9.7
-//   12 groups of 128                 8.5 / 7.1 / 9.9
-//   12 groups of 512                   - /  17 /  14
-//   64 groups of 128                  34 /  22 /  24
-//   64 groups of 256                  58 /  34 /  31
-// The few-rows form therefore for groups of at most 32 rows, or where its
-// small tiles are no more than the CUs hold at once; else 128x128 tiles until
-// they number 1.3 per CU and groups hold 192 rows.
 hipError_t launch_gemm_grouped(const GroupedGemmArgs &a, hipStream_t stream) {
-    const int64_t full = a.groups < a.M ? a.groups : a.M;
     const int cus = device_cu_count() / kXcds * kXcds;
-    const auto tiles = [&](int bm, int bn) { return (a.M + bm * full / 2) / bm * cdiv(a.N, bn); };
-    const bool few_fits = max_tiles(a.M, a.groups, kFewM) * cdiv(a.N, kFewN) < 2 * kMaxBlocks;   // of 256 threads
-    if (few_fits && (a.M <= 32 * full || 10 * tiles(kFewM, kFewN) <= 26 * cus)) return launch_few(a, stream);
-    if (10 * tiles(128, 128) <= 13 * cus || a.M < 192 * full) return launch_shape<TailShape>(a, stream);
-    const int64_t bytes = padded(a.K) / 2;
-    if (cus > 0 && a.K > 0 &&
-        stream_fits(a, (a.M + 15 * full) / 16 * 16 * bytes, a.groups * (cdiv(a.N, 16) * 16) * bytes))
-        return launch_stream(a, cus, stream);
+    switch (gemm_form(a, cus)) {
+    case GemmForm::kFewRows: return launch_few(a, stream);
+    case GemmForm::kTiles128: return launch_shape<TailShape>(a, stream);
+    case GemmForm::kPersistent: return launch_stream(a, cus, stream);
+    case GemmForm::kTiles256: break;
+    }
     return launch_shape<MainShape>(a, stream);
 }
 
-// 128x128 tiles while they number at most 1.3 per CU: 4 groups of 1200 x 1024
-// 6.8 us (persistent 8.3), 12 groups of it 12.8 (10.8).
 hipError_t launch_gemm_grouped_wgrad(const GroupedGemmArgs &a, hipStream_t stream) {
-    const int64_t full = a.groups < a.M ? a.groups : a.M;
     const int cus = device_cu_count() / kXcds * kXcds;
-    if (10 * a.groups * cdiv(a.N, 128) * cdiv(a.K, 128) <= 13 * cus) return launch_wgrad_shape<TailShape>(a, stream);
-    const int64_t bytes = (a.M + 127 * full) / 128 * 64;   // a blob's per row
-    if (cus > 0 && stream_fits(a, cdiv(a.N, 16) * 16 * bytes, cdiv(a.K, 16) * 16 * bytes))
-        return launch_wgrad_stream(a, cus, stream);
-    return launch_wgrad_shape<MainShape>(a, stream);
+    switch (wgrad_form(a, cus)) {
+    case GemmForm::kTiles128: return launch_wgrad_shape<TailShape>(a, stream);
+    case GemmForm::kPersistent: return launch_wgrad_stream(a, cus, stream);
+    default: return launch_wgrad_shape<MainShape>(a, stream);
+    }
 }
 
 }  // namespace mx

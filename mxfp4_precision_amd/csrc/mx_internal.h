@@ -104,8 +104,6 @@ hipError_t launch_quantize_fp8(const uint16_t *x, int64_t M, int64_t N, int64_t 
 hipError_t launch_layout_convert(bool to_tiled, int64_t rows, int64_t length, const uint8_t *q_src,
                                  const uint8_t *s_src, uint8_t *q_dst, uint8_t *s_dst, hipStream_t stream);
 hipError_t launch_quantize_grouped(const QuantArgs &a, bool dual, hipStream_t stream);
-bool grouped_gemm_fits(int64_t M, int64_t N, int groups);
-bool grouped_wgrad_fits(int64_t N, int64_t K, int groups);
 hipError_t launch_gemm_grouped(const GroupedGemmArgs &a, hipStream_t stream);
 hipError_t launch_gemm_grouped_wgrad(const GroupedGemmArgs &a, hipStream_t stream);
 int64_t adamw_chunks(int64_t numel);   // workgroups that numel elements take

@@ -50,6 +50,7 @@
 // |y| 2^(127-c).
 
 #include "grouped.h"
+#include "grouped_forms.h"
 
 namespace mx {
 namespace {
@@ -58,6 +59,7 @@ constexpr int kWaveRows = 32;
 constexpr int kTileCols = 128;
 constexpr int kWaves = 4;
 constexpr int kTileRows = kWaveRows * kWaves;
+static_assert(kTileRows == kQuantTile && kTileCols == kQuantTile, "the tile that the choice of form counts");
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
@@ -1295,8 +1297,6 @@ __device__ __forceinline__ void quantize_unit(const QuantArgs &a, const uint16_t
     *reinterpret_cast<uint32_t *>(a.s_row + ((int64_t)unit * kgroups + chunk) * 256 + slot * 4) = lane & 2 ? s23 : s01;
 }
 
-constexpr int kEarlyIndex = 256;
-
 // Wave `id` of the launch: unit id / chunks, chunk id % chunks.
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a, uint32_t chunks) {
     const int lane = threadIdx.x & 63;
@@ -1365,12 +1365,6 @@ __global__ __launch_bounds__(256) void quantize_slices_kernel(QuantArgs a, int c
               src);
     for (int chunk = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); chunk < chunks; chunk += 4)
         quantize_unit(a, src, unit, chunk, lane);
-}
-
-// Workgroups of a quantize_rows_kernel launch.
-int64_t quantize_rows_blocks(const QuantArgs &a) {
-    const int64_t full = a.groups < a.M ? a.groups : a.M;
-    return cdiv((a.M + 15 * full) / 16 * cdiv(a.N_pad, 512), 4);
 }
 
 // Both blobs of grouped rows in 128-row x 32-column tiles, for inputs whose
@@ -1567,41 +1561,32 @@ hipError_t launch_grouped(const QuantArgs &a, dim3 grid, hipStream_t stream) {
 // Grid rows: the most 128-row tiles that M rows in a.groups groups can need;
 // workgroups past those that there are return at once.
 hipError_t launch_quantize_grouped(const QuantArgs &a, bool dual, hipStream_t stream) {
-    const bool plain_rows = !dual && !a.row.use_sr && !a.row.use_2d && !a.row.rht;
-    // More gathered rows than x has: some are read again.  In us, by units in
-    // order / in slices: 512 rows of 1024 into 2 of 8 groups 6.1 / 5.7, 2048 of
-    // 2048 into 4 of 64 10.4 / 9.4, 16384 of 2048 into 2 of 16 27.1 / 22.7; into 1
-    // of 64 (8192 of 4096) 17.0 / 19.0.
-    if (plain_rows && a.row_index && a.groups <= 64 && a.M > a.x_rows && a.M > kEarlyIndex && a.N_pad > 512 &&
-        a.M < (int64_t(1) << 22)) {
+    const int chunks = (int)cdiv(a.N_pad, 512);
+    const int64_t row_tiles = quantize_row_tiles(a);
+    switch (quantize_form(a, dual, device_cu_count())) {
+    case QuantForm::kSlices: {
         // slices of about 2 MB of x
         int shift = 3;
         while (shift < 9 && (a.x_rows * a.N * 2 >> shift) > (int64_t(2) << 20)) ++shift;
-        const int64_t units = (a.M + 15 * (a.groups < a.M ? a.groups : a.M)) / 16;
+        const int64_t units = (a.M + 15 * full_groups(a.M, a.groups)) / 16;
         hipLaunchKernelGGL(quantize_slices_kernel, dim3((unsigned)(cdiv(units, kXcds) * kXcds)), dim3(256), 0, stream, a,
-                           (int)cdiv(a.N_pad, 512), shift);
+                           chunks, shift);
         return hipGetLastError();
     }
-    // (a grid holds fewer than 2^32 threads)
-    if (plain_rows && quantize_rows_blocks(a) < int64_t(1) << 24) {
+    case QuantForm::kRows:
         hipLaunchKernelGGL(quantize_rows_kernel, dim3((unsigned)quantize_rows_blocks(a)), dim3(256), 0, stream, a,
-                           (uint32_t)cdiv(a.N_pad, 512));
+                           (uint32_t)chunks);
         return hipGetLastError();
-    }
-    const int64_t full = a.groups < a.M ? a.groups : a.M;
-    QuantArgs b = a;
-    const int64_t row_tiles = (a.M + (kTileRows - 1) * full) / kTileRows;
-    // In us, 128 x 128 tiles / narrow ones, full groups: 64 tiles 6.1 / 4.2 (SR 8.0
-    // / 5.1), 256 tiles 6.3 / 7.1 (8.5 / 8.9), 512 tiles 8.4 / 10.5; but the count
-    // bounds ragged groups from above, and a training step of 558 rows in 32
-    // groups, 1472 x 1216, (432 tiles by the bound) runs 105 / 98.
-    if (dual && !a.row.rht && !a.col.rht && row_tiles * cdiv(a.N, kTileCols) <= 2 * device_cu_count()) {
+    case QuantForm::kNarrow: {
         auto kernel = a.row.use_sr ? (a.col.use_sr ? quantize_narrow_kernel<true, true> : quantize_narrow_kernel<true, false>)
                                    : (a.col.use_sr ? quantize_narrow_kernel<false, true>
                                                    : quantize_narrow_kernel<false, false>);
         hipLaunchKernelGGL(kernel, dim3((unsigned)(a.N_pad / 32), (unsigned)row_tiles), dim3(256), 0, stream, a);
         return hipGetLastError();
     }
+    case QuantForm::kTiles: break;
+    }
+    QuantArgs b = a;
     for (int64_t t0 = 0; t0 < row_tiles; t0 += kMaxRowTiles) {
         b.row_tile0 = t0;
         const dim3 grid((unsigned)cdiv(a.N, kTileCols),
