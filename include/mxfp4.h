@@ -399,7 +399,12 @@ mx_status mx_gemm_a4w4_grouped_wgrad(int64_t M, int64_t N, int64_t K, const int3
  * (lo32(n>>2), hi32(n>>2), tensor_id, 4) and key = seed, its low 16 bits for m,
  * its high 16 bits for sqrt(v); with F = the 16 bits that follow the code's
  * bits in the magnitude's binary expansion, it rounds up iff the bits + F
- * carry.  A positive sqrt(v) never becomes code 0.  A block that holds Inf or
+ * carry (unbiased in sqrt(v), so the v it stands for averages above the
+ * fp32 state's: in a stationary state by about 0.48 D / sqrt(v), D being the
+ * step between codes at sqrt(v), which is 3 to 5% for elements above 2^-14 of
+ * their block's largest sqrt(v), and 11, 26 and 75% at 4, 2 and 1 times the
+ * smallest code, 2^-16 to 2^-18 of the largest).  A positive sqrt(v) never
+ * becomes code 0.  A block that holds Inf or
  * NaN gets scale 0xFF and zero codes.  Zero bytes are the initial states.
  */
 typedef enum mx_state_dtype {
@@ -433,7 +438,11 @@ typedef struct mx_adamw_opts {
     int64_t step;          /* counted from 1 */
     double grad_scale;
     uint64_t seed;
-    int param_dtype;       /* MX_F32 or MX_BF16 (rounded to nearest even) */
+    /* MX_F32, or MX_BF16, rounded to nearest even: an update (decay included)
+     * below half a bf16 step, 2^-9 to 2^-8 of the parameter, is lost, however
+     * often it comes.  Where such updates count: fp32 parameters with a bf16
+     * param_copy. */
+    int param_dtype;
     int grad_dtype;        /* MX_F32 or MX_BF16 */
     int state_dtype;       /* mx_state_dtype */
     uint32_t use_sr;       /* MXFP8 states: stochastic rounding */

@@ -17,7 +17,10 @@
 // each step).  With beta2 near 1 a step changes sqrt(v) by less than half an
 // E4M3 step, so nearest rounding would hold it for ever: stochastic rounding
 // (16 bits of Philox-4x32-10 for each state and element) is the mode meant
-// for training.  A positive sqrt(v) keeps at least the smallest code: at 0
+// for training.  It is unbiased in sqrt(v), so the v it stands for averages
+// higher by the held value's variance: for gradients of constant variance
+// 0.48 D / sqrt(v) (D: the step between codes), 3.5% at beta2 0.99 and 4.6% at
+// 0.999, 26% at twice the smallest code.  A positive sqrt(v) keeps at least the smallest code: at 0
 // the next update would be divided by eps.
 //
 // A lane owns 8 consecutive elements, so a block's largest value is found in
