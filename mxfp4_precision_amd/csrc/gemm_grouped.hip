@@ -302,9 +302,9 @@ __global__ __launch_bounds__(C::kThreads) void gemm_grouped_wgrad_kernel(const i
 // An XCD's workgroups walk a contiguous range of the tile order round-robin,
 // so that they share A rows and B columns in its L2.  The ranges hold equally
 // many tiles, or, with WGRAD, equally much work: a tile costs its k-steps and
-// kTileCost more for its stores.  Training steps of 16384 rows in 16 groups and
-// 65536 in 32, run in turn: 409 and 1253 us (kTileCost 8: 419 and 1259, 0: 406 and
-// 1264, equally many tiles: 5% more).
+// kTileCost more for its stores.  Training steps of 16384 rows in 16 groups
+// (416 us) and 65536 in 32 (1235), run in turn with others: kTileCost 8 takes 2.4
+// and 0.5% more, 0 takes 0.7% less and 0.9% more, equally many tiles 5% more.
 constexpr int kTileCost = 4;
 
 struct StreamTile {
@@ -556,10 +556,6 @@ hipError_t launch_few(const GroupedGemmArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// The epilogue for any N and row stride (ODD).  Run in turn, the other epilogue in
-// parentheses: 20510 rows of 809 columns, stride 816, K 1204 in 7 groups 42.7 us
-// with its quantization (46.9 non-temporal); a training step of 16384 rows,
-// 4096 x 2048 in 16 groups 441 us (480 without non-temporal stores).
 hipError_t launch_stream(const GroupedGemmArgs &a, int cus, hipStream_t stream) {
     using C = Cfg<Fp4Fmt, MainShape>;
     auto kernel = odd_rows(a, a.N) ? (a.bias ? gemm_grouped_stream_kernel<C, false, true, true>

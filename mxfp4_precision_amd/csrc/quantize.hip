@@ -1339,8 +1339,10 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a, uint32_
 // units, and an XCD runs a contiguous range of slices, so that all but the
 // first read of a row finds it in that XCD's L2.  Workgroup = unit; its waves
 // take the chunks in turn.  At most 64 groups, one a lane.  16384 rows of 4096,
-// each in 4 of 64 groups: 97.7 -> 73.7 us (the same rows all in L2: 50; slices
-// of 8, 4, 2, 0.25 and 0.06 MB: 83.3, 77.1, 73.7, 73.2 and 75.1).
+// each in 4 of 64 groups: 101 -> 86 us with four inputs in turn, 96 -> 74 with
+// one input again and again, which the cache behind the L2s then holds in part
+// (the same rows all in L2: 50; slices of 8, 4, 2, 0.25 and 0.06 MB on one
+// input: 83.3, 77.1, 73.7, 73.2 and 75.1).
 __global__ __launch_bounds__(256) void quantize_slices_kernel(QuantArgs a, int chunks, int shift) {
     const int lane = threadIdx.x & 63;
     GroupCarry c;
