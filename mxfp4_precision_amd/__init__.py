@@ -34,6 +34,8 @@ MX_BF16 = 0
 MX_F32 = 1
 MX_FP6_E2M3 = 2
 MX_FP6_E3M2 = 3
+MX_FP8_E4M3 = 0
+MX_FP8_E5M2 = 1
 MX_STATE_F32 = 0
 MX_STATE_MXFP8 = 1
 
@@ -43,6 +45,8 @@ EXPORTED = ("mx_blob_bytes", "mx_quantize_rowwise", "mx_quantize_dual", "mx_gemm
             "mx_fp6_blob_bytes", "mx_quantize_fp6", "mx_gemm_fp6", "mx_quantize_dual_mul",
             "mx_grouped_blob_bytes", "mx_quantize_grouped", "mx_gemm_a4w4_grouped", "mx_gemm_a4w4_grouped_wgrad",
             "mx_adamw", "mx_adamw_step_values",
+            "mx_f8_b128_blob_bytes", "mx_quantize_fp8_b128", "mx_gemm_f8_b128", "mx_linear_f8_b128_bytes",
+            "mx_linear_f8_b128",
             "mx_measure_mfma", "mx_set_device_arch_override", "mx_status_string", "mx_last_error")
 
 
@@ -144,6 +148,11 @@ def lib() -> ctypes.CDLL:
     L.mx_gemm_a4w4_grouped_wgrad.argtypes = [i64, i64, i64, vp, i32, vp, vp, vp, vp, i32, i32, vp, i64, i64, vp]
     L.mx_adamw.argtypes = [ctypes.POINTER(mx_adamw_tensor), i64, ctypes.POINTER(mx_adamw_opts), vp]
     L.mx_adamw_step_values.argtypes = [ctypes.POINTER(mx_adamw_opts), ctypes.POINTER(mx_adamw_step)]
+    L.mx_f8_b128_blob_bytes.argtypes = [i64, i64, i32, szp, szp]
+    L.mx_quantize_fp8_b128.argtypes = [vp, i64, i64, i64, i32, optp, i32, optp, i32, vp, vp, vp, vp, vp]
+    L.mx_gemm_f8_b128.argtypes = [i32, i32, i64, i64, i64, i32, vp, vp, i32, vp, vp, i32, i32, vp, vp, i64, vp]
+    L.mx_linear_f8_b128_bytes.argtypes = [i64, i64, szp]
+    L.mx_linear_f8_b128.argtypes = [i64, i64, i64, i32, vp, i64, i32, vp, vp, i32, i32, vp, vp, i64, vp, vp]
     L.mx_dequantize.argtypes = [vp, vp, i64, i64, i32, vp, i64, vp]
     L.mx_measure_mfma.argtypes = [i32, i32, vp, i32, i64, vp, vp]
     L.mx_set_device_arch_override.argtypes = [ctypes.c_char_p]
@@ -197,6 +206,14 @@ def _i32ptr(p, count: int) -> Optional[int]:
             raise TypeError("a contiguous int32 tensor of at least %d values is required, got %s of %s"
                             % (count, p.dtype, tuple(p.shape)))
     return _dptr(p)
+
+
+def _room(workspace, need, *sizes):
+    """A tensor given as workspace has need(*sizes) bytes at least (an int's caller vouches for it)."""
+    if workspace is not None and not isinstance(workspace, int) and hasattr(workspace, "data_ptr"):
+        have = workspace.numel() * workspace.element_size()
+        if not workspace.is_contiguous() or have < need(*sizes):
+            raise ValueError("the workspace needs %d contiguous bytes, the tensor has %d" % (need(*sizes), have))
 
 
 def _hptr(p) -> Optional[int]:
@@ -312,6 +329,38 @@ def mx_gemm_f8_tw(transA: int, transB: int, M: int, N: int, K: int, A, a_scale_i
                                _dptr(b_scale_inv), layout, out_dtype, _dptr(C), ldc, _stream(stream)))
 
 
+def mx_f8_b128_blob_bytes(rows: int, length: int, layout: int) -> Tuple[int, int]:
+    d, s = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().mx_f8_b128_blob_bytes(rows, length, layout, ctypes.byref(d), ctypes.byref(s)))
+    return d.value, s.value
+
+
+def mx_quantize_fp8_b128(x, M: int, N: int, ldx: int, row_fmt: int, row_opts, col_fmt: int, col_opts, layout: int,
+                         q_row, s_row, q_col=None, s_col=None, stream=None):
+    _check(lib().mx_quantize_fp8_b128(_dptr(x), M, N, ldx, row_fmt, _opts(row_opts), col_fmt, _opts(col_opts), layout,
+                                      _dptr(q_row), _dptr(s_row), _dptr(q_col), _dptr(s_col), _stream(stream)))
+
+
+def mx_gemm_f8_b128(transA: int, transB: int, M: int, N: int, K: int, fmt_a: int, A, A_scale, fmt_b: int, B, B_scale,
+                    layout: int, out_dtype: int, bias, C, ldc: int, stream=None):
+    _check(lib().mx_gemm_f8_b128(transA, transB, M, N, K, fmt_a, _dptr(A), _dptr(A_scale), fmt_b, _dptr(B),
+                                 _dptr(B_scale), layout, out_dtype, _dptr(bias), _dptr(C), ldc, _stream(stream)))
+
+
+def mx_linear_f8_b128_bytes(M: int, K: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().mx_linear_f8_b128_bytes(M, K, ctypes.byref(n)))
+    return n.value
+
+
+def mx_linear_f8_b128(M: int, N: int, K: int, fmt_x: int, x, ldx: int, fmt_w: int, W, W_scale, layout: int,
+                      out_dtype: int, bias, y, ldy: int, workspace, stream=None):
+    """workspace: a tensor or pointer of mx_linear_f8_b128_bytes(M, K) bytes; a shorter tensor is refused."""
+    _room(workspace, mx_linear_f8_b128_bytes, M, K)
+    _check(lib().mx_linear_f8_b128(M, N, K, fmt_x, _dptr(x), ldx, fmt_w, _dptr(W), _dptr(W_scale), layout, out_dtype,
+                                   _dptr(bias), _dptr(y), ldy, _dptr(workspace), _stream(stream)))
+
+
 def mx_grouped_blob_bytes(M: int, N: int, groups: int) -> Tuple[int, int, int, int]:
     """(row data, row scales, column data, column scales): the most bytes that M rows in `groups` groups need."""
     n = [ctypes.c_size_t() for _ in range(4)]
@@ -418,3 +467,10 @@ def empty_grouped_blob(M: int, N: int, groups: int, device="cuda"):
     elements into `groups` groups."""
     import torch
     return tuple(torch.empty(max(n, 1), dtype=torch.uint8, device=device) for n in mx_grouped_blob_bytes(M, N, groups))
+
+
+def empty_f8_b128_blob(rows: int, length: int, layout: int, device="cuda"):
+    """Allocate (data, scale) uint8 tensors of one FP8 blob with block scales of 128."""
+    import torch
+    return tuple(torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+                 for n in mx_f8_b128_blob_bytes(rows, length, layout))

@@ -10,6 +10,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include "gemm_f8_b128_forms.h"
 #include "grouped_forms.h"
 #include "mx_internal.h"
 
@@ -428,6 +429,156 @@ mx_status mx_gemm_f8_tw(int transA, int transB, int64_t M, int64_t N, int64_t K,
                                             static_cast<const uint8_t *>(B), b_scale_inv, out_dtype, C, ldc,
                                             stream),
                         "mx_gemm_f8_tw");
+}
+
+namespace {
+
+mx_status check_f8_fmt(int fmt, const char *which) {
+    if (fmt != MX_FP8_E4M3 && fmt != MX_FP8_E5M2)
+        return fail(MX_ERR_UNSUPPORTED, "%s element format %d (valid: MX_FP8_E4M3=0, MX_FP8_E5M2=1)", which, fmt);
+    return MX_SUCCESS;
+}
+
+mx_status check_f8_opts(const mx_quant_opts *o, const char *which) {
+    MX_TRY(check_opts(o, which));
+    if (o && (o->use_sr || o->rht))
+        return fail(MX_ERR_UNSUPPORTED, "%s options: use_sr and rht are not available for blocks of 128", which);
+    return MX_SUCCESS;
+}
+
+// What the product checks of everything but its operands.
+mx_status check_f8_product(const char *name, int64_t M, int64_t N, int64_t K, int fmt_a, int fmt_b, mx_layout layout,
+                           mx_dtype out_dtype, const void *bias, const void *C, int64_t ldc) {
+    if (M < 0 || N < 0 || K < 0)
+        return fail(MX_ERR_INVALID_ARGUMENT, "negative shape M=%lld N=%lld K=%lld", (long long)M, (long long)N,
+                    (long long)K);
+    MX_TRY(check_f8_fmt(fmt_a, "A"));
+    MX_TRY(check_f8_fmt(fmt_b, "B"));
+    MX_TRY(check_layout(layout));
+    if (layout != MX_LAYOUT_TILED) return fail(MX_ERR_UNSUPPORTED, "%s reads MX_LAYOUT_TILED blobs only", name);
+    if (out_dtype != MX_BF16 && out_dtype != MX_F32)
+        return fail(MX_ERR_UNSUPPORTED, "out_dtype %d (valid: MX_BF16=0, MX_F32=1)", (int)out_dtype);
+    if (ldc < N || ldc < 1) return fail(MX_ERR_INVALID_ARGUMENT, "ldc=%lld must be >= max(N, 1)", (long long)ldc);
+    if (!C) return fail(MX_ERR_INVALID_ARGUMENT, "C is NULL");
+    if (!aligned16(C) || !aligned16(bias)) return fail(MX_ERR_MISALIGNED, "bias and C must be 16-byte aligned");
+    if (ldc % 8) return fail(MX_ERR_MISALIGNED, "ldc=%lld must be a multiple of 8", (long long)ldc);
+    // (sizes whose products could pass 64 bits)
+    constexpr int64_t kMost = int64_t(1) << 40;
+    if (M >= kMost || N >= kMost || K >= kMost / 2)
+        return fail(MX_ERR_UNSUPPORTED, "%s: M=%lld N=%lld K=%lld is too large", name, (long long)M, (long long)N,
+                    (long long)K);
+    if (K > 0) {
+        // (rows * K_pad by division: it can pass 64 bits)
+        const int64_t K_pad = mx::padded(K), rows = M > N ? M : N;
+        if (mx::cdiv(rows, 16) * 16 > ((int64_t(1) << 31) - 1) / K_pad)
+            return fail(MX_ERR_UNSUPPORTED,
+                        "%s: an operand blob of %lld rows of %lld bytes; operand blobs are addressed with 32-bit "
+                        "offsets and must stay below 2 GiB (split the product along M, N or K)",
+                        name, (long long)rows, (long long)K_pad);
+    }
+    if (!mx::f8_gemm_fits(M, N))
+        return fail(MX_ERR_UNSUPPORTED, "%s: M=%lld N=%lld needs too many output tiles", name, (long long)M,
+                    (long long)N);
+    return MX_SUCCESS;
+}
+
+}  // namespace
+
+mx_status mx_f8_b128_blob_bytes(int64_t rows, int64_t length, mx_layout layout, size_t *data_bytes,
+                                size_t *scale_bytes) {
+    MX_TRY(mx_fp8_blob_bytes(rows, length, layout, data_bytes));
+    const int64_t nb = mx::cdiv(length, 128);
+    if (scale_bytes)
+        *scale_bytes = (size_t)(layout == MX_LAYOUT_TILED ? mx::cdiv(rows, 16) * mx::cdiv(nb, 4) * 64 : rows * nb);
+    return MX_SUCCESS;
+}
+
+mx_status mx_quantize_fp8_b128(const void *x, int64_t M, int64_t N, int64_t ldx, int row_fmt,
+                               const mx_quant_opts *row_opts, int col_fmt, const mx_quant_opts *col_opts,
+                               mx_layout layout, void *q_row, void *s_row, void *q_col, void *s_col,
+                               hipStream_t stream) {
+    const bool row = q_row || s_row, col = q_col || s_col;
+    MX_TRY(validate_x(x, M, N, ldx));
+    if (!row && !col) return fail(MX_ERR_INVALID_ARGUMENT, "the outputs of both directions are NULL");
+    if (row) {
+        MX_TRY(check_f8_fmt(row_fmt, "row"));
+        MX_TRY(check_f8_opts(row_opts, "row"));
+    }
+    if (col) {
+        MX_TRY(check_f8_fmt(col_fmt, "col"));
+        MX_TRY(check_f8_opts(col_opts, "col"));
+    }
+    MX_TRY(check_layout(layout));
+    if (row) MX_TRY(validate_out(q_row, s_row, "row-wise"));
+    if (col) MX_TRY(validate_out(q_col, s_col, "column-wise"));
+    if (M == 0 || N == 0) return MX_SUCCESS;
+    if (mx::cdiv(M, 128) > (mx::kF8MaxBlocks - 1) / mx::cdiv(N, 128))
+        return fail(MX_ERR_UNSUPPORTED, "M=%lld N=%lld: 2^23 or more tiles of 128 x 128", (long long)M, (long long)N);
+    MX_TRY(check_device());
+    const mx::F8QuantArgs a{static_cast<const uint16_t *>(x), M, N, ldx, row_fmt, col_fmt,
+                            row && row_opts && row_opts->use_2d_block, col && col_opts && col_opts->use_2d_block,
+                            static_cast<uint8_t *>(q_row), static_cast<uint8_t *>(s_row),
+                            static_cast<uint8_t *>(q_col), static_cast<uint8_t *>(s_col)};
+    return check_launch(mx::launch_quantize_f8_b128(a, layout, stream), "mx_quantize_fp8_b128");
+}
+
+mx_status mx_gemm_f8_b128(int transA, int transB, int64_t M, int64_t N, int64_t K, int fmt_a, const void *A,
+                          const void *A_scale, int fmt_b, const void *B, const void *B_scale, mx_layout layout,
+                          mx_dtype out_dtype, const void *bias, void *C, int64_t ldc, hipStream_t stream) {
+    const char *name = "mx_gemm_f8_b128";
+    if (transA != 0 || transB != 1)
+        return fail(MX_ERR_UNSUPPORTED, "transA=%d transB=%d: only transA=0, transB=1 (C = A . B^T) is supported",
+                    transA, transB);
+    MX_TRY(check_f8_product(name, M, N, K, fmt_a, fmt_b, layout, out_dtype, bias, C, ldc));
+    if (K > 0 && (!A || !A_scale || !B || !B_scale))
+        return fail(MX_ERR_INVALID_ARGUMENT, "operand pointer is NULL");
+    if (K > 0 && (!aligned16(A) || !aligned16(A_scale) || !aligned16(B) || !aligned16(B_scale)))
+        return fail(MX_ERR_MISALIGNED, "operands must be 16-byte aligned");
+    if (M == 0 || N == 0) return MX_SUCCESS;
+    MX_TRY(check_device());
+    const mx::F8GemmArgs a{M, N, K, fmt_a, fmt_b, static_cast<const uint8_t *>(A),
+                           static_cast<const uint8_t *>(A_scale), static_cast<const uint8_t *>(B),
+                           static_cast<const uint8_t *>(B_scale), static_cast<const uint16_t *>(bias), out_dtype, C,
+                           ldc};
+    return check_launch(mx::launch_gemm_f8_b128(a, stream), name);
+}
+
+mx_status mx_linear_f8_b128_bytes(int64_t M, int64_t K, size_t *bytes) {
+    size_t data, scale;
+    MX_TRY(mx_f8_b128_blob_bytes(M, K, MX_LAYOUT_TILED, &data, &scale));
+    if (!bytes) return fail(MX_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    *bytes = data + scale;   // (data: whole kilobytes, so the scales are aligned)
+    return MX_SUCCESS;
+}
+
+mx_status mx_linear_f8_b128(int64_t M, int64_t N, int64_t K, int fmt_x, const void *x, int64_t ldx, int fmt_w,
+                            const void *W, const void *W_scale, mx_layout layout, mx_dtype out_dtype, const void *bias,
+                            void *y, int64_t ldy, void *workspace, hipStream_t stream) {
+    const char *name = "mx_linear_f8_b128";
+    MX_TRY(check_f8_product(name, M, N, K, fmt_x, fmt_w, layout, out_dtype, bias, y, ldy));
+    size_t data = 0;
+    if (K > 0) {
+        MX_TRY(validate_x(x, M, K, ldx));
+        if (!W || !W_scale) return fail(MX_ERR_INVALID_ARGUMENT, "W or its scales are NULL");
+        if (!aligned16(W) || !aligned16(W_scale)) return fail(MX_ERR_MISALIGNED, "W must be 16-byte aligned");
+        size_t bytes;
+        MX_TRY(mx_linear_f8_b128_bytes(M, K, &bytes));
+        if (bytes && !workspace) return fail(MX_ERR_INVALID_ARGUMENT, "workspace is NULL (%zu bytes)", bytes);
+        if (!aligned16(workspace)) return fail(MX_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+        MX_TRY(mx_f8_b128_blob_bytes(M, K, MX_LAYOUT_TILED, &data, nullptr));
+    }
+    if (M == 0 || N == 0) return MX_SUCCESS;
+    MX_TRY(check_device());
+    uint8_t *q = static_cast<uint8_t *>(workspace);
+    const mx::F8GemmArgs g{M, N, K, fmt_x, fmt_w, q, q + data, static_cast<const uint8_t *>(W),
+                           static_cast<const uint8_t *>(W_scale), static_cast<const uint16_t *>(bias), out_dtype, y,
+                           ldy};
+    if (K > 0) {
+        const mx::F8QuantArgs a{static_cast<const uint16_t *>(x), M, K, ldx, fmt_x, 0, false, false, q, q + data,
+                                nullptr, nullptr};
+        MX_TRY(check_launch(mx::launch_quantize_f8_b128(a, MX_LAYOUT_TILED, stream), name));
+    }
+    return check_launch(mx::launch_gemm_f8_b128(g, stream), name);
 }
 
 namespace {

@@ -55,6 +55,30 @@ struct GroupedGemmArgs {
     int64_t ldc, group_stride;
 };
 
+// FP8 with a scale for each block of 128.
+struct F8QuantArgs {
+    const uint16_t *x;
+    int64_t M, N, ldx;
+    int fmt_row, fmt_col;       // mx_fp8_format
+    bool row_2d, col_2d;        // 128 x 128 tiles share a scale
+    uint8_t *q_row, *s_row, *q_col, *s_col;   // either pair may be NULL
+};
+struct F8GemmArgs {
+    int64_t M, N, K;
+    int fmt_a, fmt_b;
+    const uint8_t *A, *As, *B, *Bs;
+    const uint16_t *bias;       // N, or NULL
+    mx_dtype out_dtype;
+    void *C;
+    int64_t ldc;
+};
+// mx_linear_f8_b128: the A of the product is x, quantized on the way.
+struct F8LinearArgs {
+    const uint16_t *x;
+    int64_t ldx;
+    F8GemmArgs g;               // A, As: the workspace's blob, if the form needs one
+};
+
 // Descriptors of one AdamW launch, passed as kernel arguments.
 struct AdamwItem {
     void *param;
@@ -101,6 +125,8 @@ hipError_t launch_gemm_fp8(int64_t M, int64_t N, int64_t K, const uint8_t *A, co
                            hipStream_t stream);
 hipError_t launch_quantize_fp8(const uint16_t *x, int64_t M, int64_t N, int64_t ldx, mx_layout layout,
                                uint8_t *q_row, uint8_t *q_col, float *info, hipStream_t stream);
+hipError_t launch_quantize_f8_b128(const F8QuantArgs &a, mx_layout layout, hipStream_t stream);
+hipError_t launch_gemm_f8_b128(const F8GemmArgs &a, hipStream_t stream);
 hipError_t launch_layout_convert(bool to_tiled, int64_t rows, int64_t length, const uint8_t *q_src,
                                  const uint8_t *s_src, uint8_t *q_dst, uint8_t *s_dst, hipStream_t stream);
 hipError_t launch_quantize_grouped(const QuantArgs &a, bool dual, hipStream_t stream);

@@ -1,0 +1,123 @@
+"""FP8 with block scales of 128 on the CPU: blob sizes, refusals before any launch, and the form a size takes."""
+import ctypes
+
+import pytest
+
+import mxfp4_precision_amd as mx
+
+A16 = 1 << 20
+T, C = mx.MX_LAYOUT_TILED, mx.MX_LAYOUT_CANONICAL
+OK = mx.MX_ERR_DEVICE_UNSUPPORTED    # passed every check
+INVALID, MISALIGNED, UNSUPPORTED = mx.MX_ERR_INVALID_ARGUMENT, mx.MX_ERR_MISALIGNED, mx.MX_ERR_UNSUPPORTED
+
+
+@pytest.fixture(autouse=True)
+def _no_launch():
+    """The addresses here are never real: every valid call stops at the device check."""
+    mx.mx_set_device_arch_override("gfx000")
+    yield
+    mx.mx_set_device_arch_override(None)
+
+
+def status(fn, *args):
+    try:
+        fn(*args)
+        return mx.MX_SUCCESS
+    except mx.MXError as e:
+        return e.status
+
+
+def quantize(**kw):
+    a = dict(x=A16, M=40, N=300, ldx=304, fr=0, ro=None, fc=1, co=None, layout=T, q=A16, s=A16, qc=A16, sc=A16)
+    a.update(kw)
+    return status(mx.mx_quantize_fp8_b128, *a.values(), 0)
+
+
+def gemm(**kw):
+    a = dict(ta=0, tb=1, M=40, N=300, K=200, fa=0, A=A16, As=A16, fb=1, B=A16, Bs=A16, layout=T, dt=mx.MX_BF16,
+             bias=None, C=A16, ldc=304)
+    a.update(kw)
+    return status(mx.mx_gemm_f8_b128, *a.values(), 0)
+
+
+def linear(**kw):
+    a = dict(M=40, N=300, K=200, fx=0, x=A16, ldx=200, fw=0, W=A16, Ws=A16, layout=T, dt=mx.MX_BF16, bias=None, y=A16,
+             ldy=304, ws=A16)
+    a.update(kw)
+    return status(mx.mx_linear_f8_b128, *a.values(), 0)
+
+
+def test_blob_sizes():
+    assert mx.mx_f8_b128_blob_bytes(40, 300, C) == (40 * 384, 40 * 3)
+    assert mx.mx_f8_b128_blob_bytes(40, 300, T) == (48 * 384, 3 * 64)
+    assert mx.mx_f8_b128_blob_bytes(1, 1, T) == (16 * 128, 64)
+    assert mx.mx_f8_b128_blob_bytes(16, 513, T) == (16 * 640, 2 * 64)
+    assert mx.mx_f8_b128_blob_bytes(0, 5, T) == (0, 0) == mx.mx_f8_b128_blob_bytes(5, 0, C)
+    assert status(mx.mx_f8_b128_blob_bytes, -1, 5, T) == INVALID
+    assert status(mx.mx_f8_b128_blob_bytes, 1, 5, 7) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw,want", [
+    ({}, OK), (dict(q=0, s=0), OK), (dict(qc=0, sc=0), OK), (dict(layout=C), OK),
+    (dict(q=0, s=0, fr=9, ro=mx.quant_opts(use_sr=True)), OK), (dict(qc=0, sc=0, fc=9), OK),
+    (dict(ro=mx.quant_opts(use_2d_block=True), co=mx.quant_opts(use_2d_block=True)), OK),
+    (dict(q=0, s=0, qc=0, sc=0), INVALID), (dict(q=0), INVALID), (dict(sc=0), INVALID), (dict(x=0), INVALID),
+    (dict(M=-1), INVALID), (dict(N=-1), INVALID), (dict(ldx=296), INVALID),
+    (dict(ldx=308), MISALIGNED), (dict(x=A16 + 8), MISALIGNED), (dict(q=A16 + 4), MISALIGNED),
+    (dict(fr=2), UNSUPPORTED), (dict(fc=-1), UNSUPPORTED), (dict(layout=2), UNSUPPORTED),
+    (dict(ro=mx.quant_opts(use_sr=True)), UNSUPPORTED), (dict(co=mx.quant_opts(rht=5)), UNSUPPORTED),
+    (dict(M=1 << 20, N=1 << 17, ldx=1 << 17), UNSUPPORTED), (dict(M=1 << 62, N=1 << 40, ldx=1 << 40), UNSUPPORTED),
+    (dict(M=(1 << 20) - 128, N=1 << 17, ldx=1 << 17), OK),
+    (dict(M=0), mx.MX_SUCCESS), (dict(N=0), mx.MX_SUCCESS),
+], ids=str)
+def test_quantizer_checks(kw, want):
+    assert quantize(**kw) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    ({}, OK), (dict(bias=A16), OK), (dict(dt=mx.MX_F32), OK), (dict(K=0, A=0, As=0, B=0, Bs=0), OK),
+    (dict(ta=1), UNSUPPORTED), (dict(tb=0), UNSUPPORTED), (dict(layout=C), UNSUPPORTED), (dict(fa=2), UNSUPPORTED),
+    (dict(fb=-1), UNSUPPORTED), (dict(dt=5), UNSUPPORTED),
+    (dict(M=-1), INVALID), (dict(K=-1), INVALID), (dict(ldc=299), INVALID), (dict(C=0), INVALID), (dict(Bs=0), INVALID),
+    (dict(A=0), INVALID), (dict(ldc=300), MISALIGNED), (dict(bias=A16 + 2), MISALIGNED), (dict(As=A16 + 8), MISALIGNED),
+    (dict(M=1 << 24, K=128), UNSUPPORTED), (dict(M=(1 << 24) - 16, K=128), OK), (dict(N=1 << 14, ldc=1 << 14, K=1 << 17), UNSUPPORTED),
+    (dict(N=(1 << 14) - 16, ldc=1 << 14, K=1 << 17), OK),
+    (dict(M=1 << 62, K=1 << 62), UNSUPPORTED), (dict(M=1 << 39, K=0), UNSUPPORTED),
+    (dict(M=1 << 23, N=1 << 23, ldc=1 << 23, K=128), UNSUPPORTED),
+    (dict(M=0), mx.MX_SUCCESS), (dict(N=0), mx.MX_SUCCESS),
+], ids=str)
+def test_product_checks(kw, want):
+    assert gemm(**kw) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    ({}, OK), (dict(bias=A16), OK), (dict(K=0, x=0, W=0, Ws=0, ws=0), OK),
+    (dict(M=2000, ws=0), INVALID), (dict(M=2000, ws=A16 + 8), MISALIGNED), (dict(x=0), INVALID), (dict(W=0), INVALID),
+    (dict(ldx=192), INVALID), (dict(ldx=204), MISALIGNED), (dict(x=A16 + 2), MISALIGNED), (dict(W=A16 + 1), MISALIGNED),
+    (dict(fx=4), UNSUPPORTED), (dict(layout=C), UNSUPPORTED), (dict(ldy=296), INVALID), (dict(y=0), INVALID),
+    (dict(M=1 << 60, K=1 << 30, ldx=1 << 30), UNSUPPORTED),
+    (dict(M=0), mx.MX_SUCCESS), (dict(N=0), mx.MX_SUCCESS),
+], ids=str)
+def test_linear_checks(kw, want):
+    assert linear(**kw) == want
+
+
+def test_linear_workspace():
+    # one blob of x at most
+    for M, K in ((1, 1), (64, 4096), (2000, 300)):
+        assert mx.mx_linear_f8_b128_bytes(M, K) in (0, sum(mx.mx_f8_b128_blob_bytes(M, K, T)))
+    assert mx.mx_linear_f8_b128_bytes(2000, 300) > 0
+    assert mx.mx_linear_f8_b128_bytes(0, 300) == 0 == mx.mx_linear_f8_b128_bytes(300, 0)
+    assert status(mx.mx_linear_f8_b128_bytes, -1, 3) == INVALID
+    assert mx.lib().mx_linear_f8_b128_bytes(1, 1, ctypes.POINTER(ctypes.c_size_t)()) == INVALID
+
+
+def test_tensors_on_the_host_and_short_workspaces_are_refused():
+    torch = pytest.importorskip("torch")
+    t = torch.zeros(1 << 16, dtype=torch.uint8)
+    with pytest.raises(TypeError):
+        quantize(x=t)
+    with pytest.raises(TypeError):
+        gemm(bias=t)
+    with pytest.raises(ValueError):
+        linear(M=2000, ws=t)

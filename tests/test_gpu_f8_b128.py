@@ -1,0 +1,195 @@
+"""GPU parity of FP8 with block scales of 128: blobs byte for byte with the 64-bit definition, products within the bar
+that follows from the matrix instruction's accumulation (gpu_util.group_model_tau)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import mxfp4_precision_amd as mx
+from mxfp4_precision_amd import synth
+
+import f8_ref as ref
+from gpu_util import host, log, to_dev_bf16
+
+pytestmark = pytest.mark.gpu
+T, C = mx.MX_LAYOUT_TILED, mx.MX_LAYOUT_CANONICAL
+FMTS = [mx.MX_FP8_E4M3, mx.MX_FP8_E5M2]
+
+
+@pytest.fixture(autouse=True)
+def _require_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def blob(rows, length, layout):
+    """Outputs with a pattern in them and 16 bytes behind each that must stay."""
+    return [torch.full((n + 16,), 0xA5, dtype=torch.uint8, device="cuda")
+            for n in mx.mx_f8_b128_blob_bytes(rows, length, layout)]
+
+
+def quantize(bits, fr, fc, layout=T, row=True, col=True, row2d=False, col2d=False, ldx=None, stream=None):
+    M, N = bits.shape
+    x, ldx = to_dev_bf16(bits, ldx)
+    r = blob(M, N, layout) if row else (None, None)
+    c = blob(N, M, layout) if col else (None, None)
+    mx.mx_quantize_fp8_b128(x, M, N, ldx, fr, mx.quant_opts(use_2d_block=row2d), fc, mx.quant_opts(use_2d_block=col2d),
+                            layout, *r, *c, stream)
+    return r, c
+
+
+def check_blob(got, bits, direction, fmt, layout, use_2d, what):
+    want = ref.quantize(bits, direction, fmt, use_2d)
+    if layout == T:
+        want = ref.to_tiled(*want)
+    for g, w, name in zip(got, want, ("codes", "scales")):
+        g, w = host(g), w.reshape(-1)
+        assert (g[w.size:] == 0xA5).all(), what + ": written past the end of the " + name
+        bad = np.flatnonzero(g[:w.size] != w)
+        assert bad.size == 0, (what, name, bad.size, bad[:4], g[bad[:4]], w[bad[:4]])
+
+
+def wild(M, N, seed=0):
+    """Values of very different size from block to block, zeros, subnormals, Inf and NaN in a few blocks."""
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((M, N)) * np.exp2(rng.integers(-20, 20, (M, 1)))
+    x *= np.exp2(rng.integers(-8, 8, (1, N)))
+    b = synth.bf16_bits(x.astype(np.float32)).reshape(M, N)
+    b[rng.random((M, N)) < 0.05] = 0x8000
+    b[:, N // 3:N // 3 + 1] = 0
+    b[M // 2] = rng.integers(0, 0x0100, N).astype(np.uint16)          # subnormals and the smallest normals
+    b[M // 4] &= 0x807F
+    if M * N > 300:
+        b[M - 1, N - 1], b[0, N // 2], b[M // 5, 0] = 0x7F80, 0x7FC1, 0xFF80
+    return b
+
+
+SHAPES = [(1, 1), (1, 128), (1, 1000), (16, 128), (17, 130), (128, 128), (129, 257), (300, 72), (5, 1024), (1030, 5),
+          (256, 640), (127, 513)]
+
+
+@pytest.mark.parametrize("layout", [T, C])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_quantize_both_directions(shape, layout):
+    b = wild(*shape)
+    for fr, fc, r2, c2 in ((0, 0, False, False), (1, 0, True, False), (0, 1, False, True), (1, 1, False, False),
+                           (0, 0, True, True)):
+        r, c = quantize(b, fr, fc, layout, row2d=r2, col2d=c2)
+        check_blob(r, b, 0, fr, layout, r2, "row %s %d" % (shape, fr))
+        check_blob(c, b, 1, fc, layout, c2, "col %s %d" % (shape, fc))
+
+
+@pytest.mark.parametrize("layout", [T, C])
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("use_2d", [False, True])
+def test_quantize_one_direction(fmt, layout, use_2d):
+    for shape in ((1, 4096), (40, 333), (200, 128)):
+        b = wild(*shape, seed=3)
+        r, _ = quantize(b, fmt, 99, layout, col=False, row2d=use_2d, ldx=(shape[1] + 7) // 8 * 8 + 24)
+        check_blob(r, b, 0, fmt, layout, use_2d, "row only")
+        _, c = quantize(b, 99, fmt, layout, row=False, col2d=use_2d)
+        check_blob(c, b, 1, fmt, layout, use_2d, "col only")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_every_bf16_value(fmt):
+    """All finite values as elements, each block led by a largest value a few powers of two above them, and all of them
+    as the largest value."""
+    v = np.arange(0x7F80, dtype=np.uint16)
+    v = np.concatenate([v, v | 0x8000])
+    for up in (0, 1, 3, 7, 9, 12, 17, 30):
+        rows = np.zeros((-(-v.size // 127), 128), np.uint16)
+        rows[:, 1:].reshape(-1)[:] = np.resize(v, rows[:, 1:].size)
+        mag = (rows & 0x7FFF).max(axis=1).astype(np.int64)
+        rows[:, 0] = np.minimum(mag + (up << 7), 0x7F7F)
+        r, c = quantize(rows, fmt, fmt)
+        check_blob(r, rows, 0, fmt, T, False, "up %d" % up)
+    alone = np.zeros((v.size, 128), np.uint16)
+    alone[:, 5] = v
+    r, _ = quantize(alone, fmt, fmt, col=False)
+    check_blob(r, alone, 0, fmt, T, False, "alone")
+
+
+# ------------------------------------------------------------------ products
+def dev_blob(codes, scales):
+    """Exactly as large as the library asks for."""
+    return [torch.from_numpy(v).cuda() for v in ref.to_tiled(codes, scales)]
+
+
+def codes_of(rows, length, fmt, seed, spread=3):
+    """Random codes of every kind with scales of different size."""
+    rng = np.random.default_rng(seed)
+    Lp = ref.padded(length)
+    c = np.zeros((rows, Lp), np.uint8)
+    c[:, :length] = rng.integers(0, ref.COUNT[fmt], (rows, length)) | (rng.integers(0, 2, (rows, length)) << 7)
+    s = (127 + rng.integers(-spread, spread + 1, (rows, Lp // 128))).astype(np.uint8)
+    return c, s
+
+
+def normal_codes(rows, length, fmt, seed):
+    x = np.random.default_rng(seed).standard_normal((rows, length)).astype(np.float32)
+    return ref.quantize(synth.bf16_bits(x).reshape(rows, length), 0, fmt)
+
+
+def run(a, b, M, N, K, fa, fb, dtype, bias=None, ldc=None, stream=None):
+    ldc = ldc or (N + 7) // 8 * 8
+    out = torch.full((M + 1, ldc), -7.0, dtype=torch.float32 if dtype == mx.MX_F32 else torch.bfloat16, device="cuda")
+    mx.mx_gemm_f8_b128(0, 1, M, N, K, fa, *a, fb, *b, T, dtype, bias, out, ldc, stream)
+    got = out.double().cpu().numpy()
+    assert (got[M:] == -7).all() and (got[:, N:] == -7).all(), "written outside C"
+    return got[:M, :N], out
+
+
+def check_entries(got, want, ii, jj, tau, bias=None, what=""):
+    """Every entry within 1/8 of its row's and column's scale (a misplaced one is not), those of (ii, jj) within their
+    bars; the bias adds one fp32 rounding."""
+    g, w = got[ii, jj], want[ii, jj]
+    if bias is not None:
+        w = w + bias[jj]
+        tau = tau + 2.0 ** -23 * np.abs(w)
+    err = np.abs(g - w)
+    log("%s %s: error / bar %.3g" % (what, got.shape, (err / np.maximum(tau, 1e-300)).max()))
+    assert (err <= tau).all(), (what, got.shape, np.argwhere(err > tau)[:3], err.max())
+    full = want if bias is None else want + bias
+    size = np.sqrt((full ** 2).mean(axis=1))[:, None] + np.sqrt((full ** 2).mean(axis=0))
+    assert (np.abs(got - full) <= size / 8).all(), what
+
+
+def check_product(M, N, K, fa, fb, make, with_bias=False, what=""):
+    a, b = make(M, K, fa, 1), make(N, K, fb, 2)
+    want = ref.product(a, b, fa, fb)
+    da, db = dev_blob(*a), dev_blob(*b)
+    bias = added = None
+    if with_bias:
+        bits = synth.normal(np.random.default_rng(4), (N,), 1.0).reshape(-1)
+        bias = torch.zeros(-(-N // 8) * 8, dtype=torch.int16)
+        bias[:N] = torch.from_numpy(bits.view(np.int16))
+        bias, added = bias.cuda(), ref.to_f64(bits)
+    got, out = run(da, db, M, N, K, fa, fb, mx.MX_F32, bias)
+    check_entries(got, *want, added, "%s K %d" % (what, K))
+    # bf16 output: the fp32 output rounded once
+    got16, out16 = run(da, db, M, N, K, fa, fb, mx.MX_BF16, bias)
+    assert torch.equal(out16[:M, :N], out[:M, :N].bfloat16()), what + ": bf16 is not the rounded fp32 output"
+
+
+PRODUCTS = [
+    # few rows
+    (1, 16, 128), (1, 1, 1), (3, 40, 200), (16, 256, 512), (17, 33, 640), (33, 70, 1100), (64, 96, 513), (50, 1000, 384),
+    (200, 100, 300), (1, 700, 5000),
+    # 128 x 128 tiles
+    (1500, 1500, 200), (1153, 1985, 1300), (2000, 1111, 520),
+    # 256 x 256 tiles
+    (2300, 2500, 600), (2304, 2560, 1024),
+]
+
+
+@pytest.mark.parametrize("shape", PRODUCTS, ids=str)
+def test_product(shape):
+    M, N, K = shape
+    small = M * N * K < 10 ** 7
+    for fa, fb in ((0, 0), (1, 0), (0, 1), (1, 1)) if small else ((0, 0), (1, 0)):
+        check_product(M, N, K, fa, fb, normal_codes, what="normal %d %d" % (fa, fb))
+    check_product(M, N, K, 0, 0, normal_codes, True, "bias")
+    if small:
+        for fa, fb in ((0, 0), (1, 0), (0, 1), (1, 1)):
+            check_product(M, N, K, fa, fb, codes_of, what="codes %d %d" % (fa, fb))
