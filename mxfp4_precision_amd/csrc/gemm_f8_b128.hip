@@ -52,12 +52,21 @@ __device__ __forceinline__ uint8_t *f8_scales(int which) {
     return g_lds<2 * C::kAtoms * 64, 4> + which * (C::kAtoms * 64);
 }
 
-template <class C>
+// STREAM: the workgroup runs several tiles back to back as one stream of
+// k-steps, a tile taking `steps` of them; a DMA for step steps + j fetches step j
+// of the next tile (*_next; kleft = its k-steps, 0 when there is none).
+template <class C, bool STREAM>
 struct F8Ctx {
-    __amdgpu_buffer_rsrc_t rA, rB, rAs, rBs;
+    static constexpr bool kStream = STREAM;
+    __amdgpu_buffer_rsrc_t rA, rB, rAs, rBs, rBias;
     int row[C::kLoads];            // byte offsets of this wave's atoms at k-step 0 (wave-uniform)
     uint32_t sc[C::kScaleLoads];   // per lane: byte offsets of its scale words at k-group 0
     int ksteps, kgroups, wave, lane16;
+    int row_next[STREAM ? C::kLoads : 1];
+    uint32_t sc_next[STREAM ? C::kScaleLoads : 1];
+    int steps, kleft;
+    uint32_t bias;                 // per lane: byte offset of its two bias values
+    int parity;                    // scale buffer of the tile's k-group 0
 };
 
 template <class C>
@@ -70,33 +79,46 @@ struct F8Regs {
 // DMA instruction V of k-step k into stage S, or (V >= kLoads) of the scales of
 // k-group h.  Past K the lane offset is out of range, which gives zeros; the
 // scalar one then stays inside (the range check subtracts it from the range).
-template <class C, int S, int V>
-__device__ __forceinline__ void f8_dma(const F8Ctx<C> &c, int k) {
-    const int a = C::kWaves * V + c.wave;
+template <class C, int S, int V, class X>
+__device__ __forceinline__ void f8_dma(const X &c, int k) {
+    // (hidden, so that the addresses of all stages are not held in registers)
+    int w = c.wave;
+    asm volatile("" : "+s"(w));
+    const int a = C::kWaves * V + w;
     constexpr bool isA = C::kWaves * (V + 1) <= C::kGA;
     const __amdgpu_buffer_rsrc_t rsrc = isA ? c.rA : c.rB;
-    const bool in = k < c.ksteps;
+    bool in = k < c.ksteps;
+    int row = c.row[V];
+    if constexpr (X::kStream) {
+        if (k >= c.steps) {
+            k -= c.steps;
+            in = k < c.kleft;
+            row = c.row_next[V];
+        }
+    }
     const uint32_t voff = in ? (uint32_t)c.lane16 : kOutOfRange;
-    const uint32_t soff = (uint32_t)c.row[V] + (in ? (uint32_t)k * 1024u : 0u);
+    const uint32_t soff = (uint32_t)row + (in ? (uint32_t)k * 1024u : 0u);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, MX_LDS((stage_buf<C, S, 0>() + a * 1024)), 16, voff, soff, 0, 0);
 }
-template <class C, int V>
-__device__ __forceinline__ void f8_dma_scale(const F8Ctx<C> &c, int h) {
-    const int u = C::kWaves * V + c.wave;
+template <class C, int V, class X>
+__device__ __forceinline__ void f8_dma_scale(const X &c, int h) {
+    const int u = C::kWaves * V + c.wave, to = (h + c.parity) & 1;
     const bool isA = 4 * u < C::kGA;   // wave-uniform
     const __amdgpu_buffer_rsrc_t rsrc = isA ? c.rAs : c.rBs;
-    const uint32_t voff = h < c.kgroups ? c.sc[V] + (uint32_t)h * 64u : kOutOfRange;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, MX_LDS((f8_scales<C>(h & 1) + u * 256)), 4, voff, 0, 0, 0);
+    uint32_t voff = h < c.kgroups ? c.sc[V] + (uint32_t)h * 64u : kOutOfRange;
+    if constexpr (X::kStream)
+        if (8 * h >= c.steps) voff = c.kleft > 0 ? c.sc_next[V] : kOutOfRange;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, MX_LDS((f8_scales<C>(to) + u * 256)), 4, voff, 0, 0, 0);
 }
-template <class C, int S, int V = 0>
-__device__ __forceinline__ void f8_dma_step(const F8Ctx<C> &c, int k) {
+template <class C, int S, int V = 0, class X>
+__device__ __forceinline__ void f8_dma_step(const X &c, int k) {
     if constexpr (V < C::kLoads) {
         f8_dma<C, S, V>(c, k);
         f8_dma_step<C, S, V + 1>(c, k);
     }
 }
-template <class C, int V = 0>
-__device__ __forceinline__ void f8_dma_scales(const F8Ctx<C> &c, int h) {
+template <class C, int V = 0, class X>
+__device__ __forceinline__ void f8_dma_scales(const X &c, int h) {
     if constexpr (V < C::kScaleLoads) {
         f8_dma_scale<C, V>(c, h);
         f8_dma_scales<C, V + 1>(c, h);
@@ -128,22 +150,30 @@ struct F8Off {
     int a, b, sa, sb;   // LDS byte offsets of this lane's first A and B operands and scale words
 };
 
+// LDS of a wave's bias values (stream form).
+template <class C>
+__device__ __forceinline__ uint8_t *f8_bias(int wave) {
+    return g_lds<C::kWaves * 256, 5> + wave * 256;
+}
+
 // Slot T of the k-step with position SG of 8: the MFMA, the reads of the next
 // step's operands that fall to it, the DMA instructions of step k + 3, and at
-// the end of a group of 8 the next group's scales.
-template <class C, int FA, int FB, int SG, int T>
-__device__ __forceinline__ void f8_slot(const F8Ctx<C> &c, int k, v16f (&acc)[C::kMB][C::kMA], F8Regs<C> &r,
+// the end of a group of 8 the next group's scales.  FRESH: a tile's first group
+// in the stream form, whose first step starts the accumulators from 0 and which
+// fetches the tile's bias.
+template <class C, int FA, int FB, int SG, bool FRESH, int T, class X>
+__device__ __forceinline__ void f8_slot(const X &c, int k, v16f (&acc)[C::kMB][C::kMA], F8Regs<C> &r,
                                         const F8Off &o) {
     constexpr int i = T / C::kMA, j = T % C::kMA, P = SG & 1, S = SG & 3;
     // (plain-typed locals: a builtin call on template-dependent operands does
     // not resolve in the host compilation pass)
     const v8i bop = r.b[P][i], aop = r.a[P][j];
     const int sb = (int)r.sb[i], sa = (int)r.sa[j];
-    const v16f cin = acc[i][j];
+    const v16f cin = FRESH && SG == 0 ? v16f{} : acc[i][j];
     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bop, aop, cin, FB, FA, SG / 2, sb, SG / 2, sa);
     f8_reads<C, (S + 1) & 3, P ^ 1, T * C::kReads / C::kSlots, (T + 1) * C::kReads / C::kSlots>(r, o.a, o.b);
     if constexpr (SG == 7 && T < C::kMA) {
-        const uint8_t *s = f8_scales<C>((k / 8 + 1) & 1);
+        const uint8_t *s = f8_scales<C>((k / 8 + 1 + c.parity) & 1);
         r.sa_n[T] = *reinterpret_cast<const uint32_t *>(s + o.sa + T * 128);
         if constexpr (T < C::kMB) r.sb_n[T] = *reinterpret_cast<const uint32_t *>(s + o.sb + T * 128);
     }
@@ -152,47 +182,97 @@ __device__ __forceinline__ void f8_slot(const F8Ctx<C> &c, int k, v16f (&acc)[C:
     if constexpr (d1 > d0 + 1) f8_dma<C, (S + 3) & 3, d0 + 1>(c, k + 3);
     static_assert(d1 <= d0 + 2, "DMA instructions per slot");
     if constexpr (SG == 4 && T < C::kScaleLoads) f8_dma_scale<C, T>(c, k / 8 + 1);
+    if constexpr (FRESH && SG == 4 && T == C::kScaleLoads) {
+        const __amdgpu_buffer_rsrc_t rsrc = c.rBias;
+        const uint32_t voff = c.bias;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, MX_LDS(f8_bias<C>(c.wave)), 4, voff, 0, 0, 0);
+    }
     __builtin_amdgcn_sched_barrier(0);
 }
-template <class C, int FA, int FB, int SG, int T = 0>
-__device__ __forceinline__ void f8_slots(const F8Ctx<C> &c, int k, v16f (&acc)[C::kMB][C::kMA], F8Regs<C> &r,
-                                         const F8Off &o) {
+template <class C, int FA, int FB, int SG, bool FRESH, int T = 0, class X>
+__device__ __forceinline__ void f8_slots(const X &c, int k, v16f (&acc)[C::kMB][C::kMA], F8Regs<C> &r, const F8Off &o) {
     if constexpr (T < C::kSlots) {
-        f8_slot<C, FA, FB, SG, T>(c, k, acc, r, o);
-        f8_slots<C, FA, FB, SG, T + 1>(c, k, acc, r, o);
+        f8_slot<C, FA, FB, SG, FRESH, T>(c, k, acc, r, o);
+        f8_slots<C, FA, FB, SG, FRESH, T + 1>(c, k, acc, r, o);
     }
 }
 
-// Vector memory instructions that may be outstanding at the start of step SG:
-// those of the two steps before it, but of the earlier one only what it issued
-// for step k + 2 ... that is, all that was issued after step k + 1's DMA.
+// Stores that a wave issues for a tile in the stream form.
 template <class C>
-constexpr int f8_outstanding(int SG) {
-    // step k - 1 issued step k + 2's DMA (and the scales if its position is 4)
-    return C::kLoads + (((SG + 7) & 7) == 4 ? C::kScaleLoads : 0);
+__host__ __device__ constexpr int f8_stores() {
+    return C::kWM * C::kWN * 2 / 1024;
 }
 
-// K-steps k0 .. k0 + 7, or fewer at the end of K (a multiple of two).
-template <class C, int FA, int FB, int SG = 0>
-__device__ __forceinline__ void f8_group(const F8Ctx<C> &c, int k0, v16f (&acc)[C::kMB][C::kMA], F8Regs<C> &r,
+// Vector memory instructions that may be outstanding at the start of the step
+// at position SG: all that were issued after its next step's DMA, that is step
+// k - 1's (and at positions 0 and 1 of a FRESH group the previous tile's stores,
+// which were issued between).
+template <class C>
+constexpr int f8_outstanding(int SG, bool fresh) {
+    return C::kLoads + (SG == 5 ? C::kScaleLoads + (fresh ? 1 : 0) : 0) + (fresh && SG < 2 ? f8_stores<C>() : 0);
+}
+
+// K-steps k0 .. k0 + 7, or (one tile) fewer at the end of K, a multiple of two.
+template <class C, int FA, int FB, bool FRESH, int SG = 0, class X>
+__device__ __forceinline__ void f8_group(const X &c, int k0, v16f (&acc)[C::kMB][C::kMA], F8Regs<C> &r,
                                          const F8Off &o) {
     if constexpr (SG < 8) {
-        if (SG > 0 && SG % 2 == 0 && k0 + SG >= c.ksteps) return;
+        if constexpr (!X::kStream && SG > 0 && SG % 2 == 0)
+            if (k0 + SG >= c.ksteps) return;
         // Step k + 1 has landed for this wave and, past the barrier, for all; and
         // every wave is past step k - 1, so the stage that step k + 3 goes to
         // (step k - 1's, read during step k - 2) is free.
+        static_assert(f8_outstanding<C>(SG, FRESH) <= 63, "vmcnt range");
         __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(f8_outstanding<C>(SG)) : "memory");
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(f8_outstanding<C>(SG, FRESH)) : "memory");
         __builtin_amdgcn_sched_barrier(0);
-        f8_slots<C, FA, FB, SG>(c, k0 + SG, acc, r, o);
+        f8_slots<C, FA, FB, SG, FRESH>(c, k0 + SG, acc, r, o);
         if constexpr (SG == 7) {
 #pragma unroll
             for (int t = 0; t < C::kMA; ++t) r.sa[t] = r.sa_n[t];
 #pragma unroll
             for (int t = 0; t < C::kMB; ++t) r.sb[t] = r.sb_n[t];
         }
-        f8_group<C, FA, FB, SG + 1>(c, k0, acc, r, o);
+        f8_group<C, FA, FB, FRESH, SG + 1>(c, k0, acc, r, o);
     }
+}
+
+// Scales of k-group 0 and operands of step 0, once they have landed.
+template <class C>
+__device__ __forceinline__ void f8_first(F8Regs<C> &r, const F8Off &o) {
+    const uint8_t *s = f8_scales<C>(0);
+#pragma unroll
+    for (int t = 0; t < C::kMA; ++t) r.sa[t] = *reinterpret_cast<const uint32_t *>(s + o.sa + t * 128);
+#pragma unroll
+    for (int t = 0; t < C::kMB; ++t) r.sb[t] = *reinterpret_cast<const uint32_t *>(s + o.sb + t * 128);
+    f8_reads<C, 0, 0, 0, C::kReads>(r, o.a, o.b);
+}
+
+template <class C>
+__device__ __forceinline__ F8Off f8_offsets(int wave, int lane) {
+    const int wm = wave % C::kWavesM, wn = wave / C::kWavesM;
+    const int lrow = lane & 31, lhi = lane >> 5;
+    const int frag = (lrow >> 4) * 1024 + ((lrow & 15) + 32 * lhi) * 16, word = (lrow >> 4) * 64 + (lrow & 15) * 4;
+    F8Off o = {frag + wm * C::kTA * 1024, frag + (C::kGA + wn * C::kTB) * 1024, word + wm * C::kTA * 64,
+               word + (C::kGA + wn * C::kTB) * 64};
+    // hide the offsets' known zero bits, so that constants go to the instructions' offset field
+    asm volatile("" : "+v"(o.a), "+v"(o.b), "+v"(o.sa), "+v"(o.sb));
+    return o;
+}
+
+// Offsets of a tile's atoms and scale words.  Row groups past an operand are
+// clamped to its last one: those rows of C are not stored.
+template <class C>
+__device__ __forceinline__ void f8_tile_rows(int tm, int tn, int nGA, int nGB, int ksteps, int kgroups, int wave,
+                                             int lane, int (&row)[C::kLoads], uint32_t (&sc)[C::kScaleLoads]) {
+    const auto group_of = [&](int a) {
+        return a < C::kGA ? min(tm * C::kGA + a, nGA - 1) : min(tn * C::kGB + (a - C::kGA), nGB - 1);
+    };
+#pragma unroll
+    for (int v = 0; v < C::kLoads; ++v) row[v] = group_of(C::kWaves * v + wave) * ksteps * 1024;
+#pragma unroll
+    for (int v = 0; v < C::kScaleLoads; ++v)
+        sc[v] = (uint32_t)(group_of(4 * (C::kWaves * v + wave) + (lane >> 4)) * kgroups * 64 + 4 * (lane & 15));
 }
 
 template <class C, int FA, int FB, bool OUT_BF16>
@@ -206,29 +286,22 @@ __global__ __launch_bounds__(C::kThreads) void gemm_f8_b128_kernel(int64_t M, in
                                                                    void *__restrict__ Cout, int64_t ldc) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave % C::kWavesM, wn = wave / C::kWavesM;
+    const int wn = wave / C::kWavesM;
     int tm, tn;
     tile_of(blockIdx.x, gridDim.x, tiles_m, tiles_n, group_m, tm, tn);
 
-    F8Ctx<C> c;
+    F8Ctx<C, false> c;
     c.ksteps = (int)(K_pad / 64);
     c.kgroups = (int)cdiv(K_pad, 512);
     c.wave = wave;
     c.lane16 = lane * 16;
+    c.parity = 0;
     const int nGA = (int)cdiv(M, 16), nGB = (int)cdiv(N, 16);
     c.rA = make_rsrc(A, (int64_t)nGA * c.ksteps * 1024);
     c.rB = make_rsrc(B, (int64_t)nGB * c.ksteps * 1024);
     c.rAs = make_rsrc(As, (int64_t)nGA * c.kgroups * 64);
     c.rBs = make_rsrc(Bs, (int64_t)nGB * c.kgroups * 64);
-    // row groups past an operand are clamped to its last one: those rows of C are not stored
-    const auto group_of = [&](int a) {
-        return a < C::kGA ? min(tm * C::kGA + a, nGA - 1) : min(tn * C::kGB + (a - C::kGA), nGB - 1);
-    };
-#pragma unroll
-    for (int v = 0; v < C::kLoads; ++v) c.row[v] = group_of(C::kWaves * v + wave) * c.ksteps * 1024;
-#pragma unroll
-    for (int v = 0; v < C::kScaleLoads; ++v)
-        c.sc[v] = (uint32_t)(group_of(4 * (C::kWaves * v + wave) + (lane >> 4)) * c.kgroups * 64 + 4 * (lane & 15));
+    f8_tile_rows<C>(tm, tn, nGA, nGB, c.ksteps, c.kgroups, wave, lane, c.row, c.sc);
 
     v16f acc[C::kMB][C::kMA];
 #pragma unroll
@@ -236,28 +309,15 @@ __global__ __launch_bounds__(C::kThreads) void gemm_f8_b128_kernel(int64_t M, in
 #pragma unroll
         for (int j = 0; j < C::kMA; ++j) acc[i][j] = v16f{};
 
-    const int lrow = lane & 31, lhi = lane >> 5;
-    const int frag = (lrow >> 4) * 1024 + ((lrow & 15) + 32 * lhi) * 16, word = (lrow >> 4) * 64 + (lrow & 15) * 4;
-    F8Off o = {frag + wm * C::kTA * 1024, frag + (C::kGA + wn * C::kTB) * 1024, word + wm * C::kTA * 64,
-               word + (C::kGA + wn * C::kTB) * 64};
-    // hide the offsets' known zero bits, so that constants go to the instructions' offset field
-    asm volatile("" : "+v"(o.a), "+v"(o.b), "+v"(o.sa), "+v"(o.sb));
-
+    const F8Off o = f8_offsets<C>(wave, lane);
     f8_dma_scales<C>(c, 0);
     f8_dma_step<C, 0>(c, 0);
     f8_dma_step<C, 1>(c, 1);
     f8_dma_step<C, 2>(c, 2);
     F8Regs<C> r;
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * C::kLoads) : "memory");
-    {
-        const uint8_t *s = f8_scales<C>(0);
-#pragma unroll
-        for (int t = 0; t < C::kMA; ++t) r.sa[t] = *reinterpret_cast<const uint32_t *>(s + o.sa + t * 128);
-#pragma unroll
-        for (int t = 0; t < C::kMB; ++t) r.sb[t] = *reinterpret_cast<const uint32_t *>(s + o.sb + t * 128);
-    }
-    f8_reads<C, 0, 0, 0, C::kReads>(r, o.a, o.b);
-    for (int k0 = 0; k0 < c.ksteps; k0 += 8) f8_group<C, FA, FB>(c, k0, acc, r, o);
+    f8_first<C>(r, o);
+    for (int k0 = 0; k0 < c.ksteps; k0 += 8) f8_group<C, FA, FB, false>(c, k0, acc, r, o);
     // drain the trailing (out-of-range) DMAs before LDS is reused
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
@@ -267,6 +327,141 @@ __global__ __launch_bounds__(C::kThreads) void gemm_f8_b128_kernel(int64_t M, in
         add_bias<C>(acc, bits);
     }
     store_tile<C, OUT_BF16>(acc, tm, tn, M, N, Cout, ldc, 0, wave, wave, lane);
+}
+
+// Persistent form (bf16 output): one workgroup per CU runs tiles b, b +
+// gridDim.x, ... of the tile order as one stream of k-steps.  A tile takes
+// `steps` = its k-steps rounded up to a multiple of 8; its last steps fetch the
+// next tile's first three, their scales and its first operands, so nothing
+// drains between tiles.  The epilogue stages C through stage 3 (the others hold
+// the next tile's steps), 8 KB a wave: in pass p a wave writes its MFMA row tile
+// p (32 rows x 128 columns, 16-byte chunk c of row r at c ^ r % 16) and reads it
+// back as whole 256-byte row segments, 4 rows per store.  Every wave issues
+// f8_stores() stores a tile whatever the edges (what lies outside C has an
+// offset out of range), so that the next tile's first two waits can count past
+// them; the third needs them done.  Needs N % 8 == 0 and 32-bit offsets into C.
+template <class C, bool BIAS>
+__device__ __forceinline__ void f8_store_private(const v16f (&acc)[C::kMB][C::kMA], int tm, int tn, int M, int N,
+                                                 __amdgpu_buffer_rsrc_t rC, int ldc, int wave, int lane) {
+    constexpr int kSlot = 32 * C::kWN * 2;
+    static_assert(C::kWN == 128 && kSlot * C::kWaves == C::kStageBytes, "one slot per wave fills stage 3");
+    // (hidden, so that no address is computed ahead of the tile loop and held)
+    asm volatile("" : "+v"(lane), "+s"(wave));
+    const int wm = wave % C::kWavesM, wn = wave / C::kWavesM;
+    const int lrow = lane & 31, lhi = lane >> 5;
+    const int row0 = tm * C::kBM + C::kWM * wm + (lane >> 4), col = tn * C::kBN + C::kWN * wn + 8 * (lane & 15);
+    uint8_t *slot = stage_buf<C, 3, 0>() + wave * kSlot;
+    const uint8_t *b = f8_bias<C>(wave) + 8 * lhi;
+    // every wave is done reading stage 3 (a bare barrier: a fence would also
+    // wait for the next tile's DMAs)
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+    for (int p = 0; p < C::kMA; ++p) {
+#pragma unroll
+        for (int i = 0; i < C::kMB; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = acc[i][p][4 * q + e];
+                if constexpr (BIAS) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(b + 2 * (32 * i + 8 * q));
+                    v[0] += __uint_as_float(w.x << 16);
+                    v[1] += __uint_as_float(w.x & 0xFFFF0000u);
+                    v[2] += __uint_as_float(w.y << 16);
+                    v[3] += __uint_as_float(w.y & 0xFFFF0000u);
+                }
+                *reinterpret_cast<uint2 *>(slot + lrow * 256 + (((4 * i + q) ^ (lrow & 15)) * 16) + 8 * lhi) =
+                    uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            }
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const int r = 4 * s + (lane >> 4);
+            const v4u_t v = *reinterpret_cast<const v4u_t *>(slot + r * 256 + (((lane & 15) ^ (r & 15)) * 16));
+            const int row = row0 + 32 * p + 4 * s;
+            const uint32_t off = row < M && col < N ? (uint32_t)(row * ldc + col) * 2u : kOutOfRange;
+            __builtin_amdgcn_raw_buffer_store_b128(v, rC, off, 0, kCachePolicyNT);
+        }
+    }
+}
+
+template <class C, int FA, int FB, bool BIAS>
+__global__ __launch_bounds__(C::kThreads) void gemm_f8_b128_stream_kernel(int M, int N, int K_pad, int tiles_m,
+                                                                          int tiles_n, int group_m,
+                                                                          const uint8_t *__restrict__ A,
+                                                                          const uint8_t *__restrict__ As,
+                                                                          const uint8_t *__restrict__ B,
+                                                                          const uint8_t *__restrict__ Bs,
+                                                                          const uint16_t *__restrict__ bias,
+                                                                          void *__restrict__ Cout, int ldc) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wn = wave / C::kWavesM;
+    const int P = gridDim.x, tiles = tiles_m * tiles_n;
+    F8Ctx<C, true> c;
+    c.ksteps = K_pad / 64;
+    c.kgroups = (K_pad + 511) / 512;
+    c.steps = 8 * c.kgroups;
+    c.wave = wave;
+    c.lane16 = lane * 16;
+    c.parity = 0;
+    const int nGA = (M + 15) / 16, nGB = (N + 15) / 16;
+    c.rA = make_rsrc(A, (int64_t)nGA * c.ksteps * 1024);
+    c.rB = make_rsrc(B, (int64_t)nGB * c.ksteps * 1024);
+    c.rAs = make_rsrc(As, (int64_t)nGA * c.kgroups * 64);
+    c.rBs = make_rsrc(Bs, (int64_t)nGB * c.kgroups * 64);
+    // whole 16-byte blocks, as the range check zeroes whole dwords
+    c.rBias = make_rsrc(bias, BIAS ? ((int64_t)N * 2 + 15) / 16 * 16 : 0);
+    const __amdgpu_buffer_rsrc_t rC = make_rsrc(Cout, ((int64_t)(M - 1) * ldc + N) * 2);
+
+    int vb = blockIdx.x, tm, tn, tm_next = 0, tn_next = 0;
+    const auto look_ahead = [&]() {
+        c.kleft = 0;
+        if (vb + P < tiles) {
+            tile_of(vb + P, tiles, tiles_m, tiles_n, group_m, tm_next, tn_next);
+            f8_tile_rows<C>(tm_next, tn_next, nGA, nGB, c.ksteps, c.kgroups, wave, lane, c.row_next, c.sc_next);
+            c.kleft = c.ksteps;
+        }
+    };
+    tile_of(vb, tiles, tiles_m, tiles_n, group_m, tm, tn);
+    f8_tile_rows<C>(tm, tn, nGA, nGB, c.ksteps, c.kgroups, wave, lane, c.row, c.sc);
+#pragma unroll
+    for (int v = 0; v < C::kLoads; ++v) c.row_next[v] = c.row[v];
+#pragma unroll
+    for (int v = 0; v < C::kScaleLoads; ++v) c.sc_next[v] = c.sc[v];
+    look_ahead();
+
+    const F8Off o = f8_offsets<C>(wave, lane);
+    f8_dma_scales<C>(c, 0);
+    f8_dma_step<C, 0>(c, 0);
+    f8_dma_step<C, 1>(c, 1);
+    f8_dma_step<C, 2>(c, 2);
+    F8Regs<C> r;
+    // all of it, so that the first tile's first two waits, which count past
+    // stores that it does not have, need not wait; as a builtin, so that the
+    // compiler's own wait tracking knows too
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+    __builtin_amdgcn_s_barrier();
+    f8_first<C>(r, o);
+    v16f acc[C::kMB][C::kMA];
+    for (;;) {
+        c.bias = (uint32_t)(tn * C::kBN + wn * C::kWN + 2 * lane) * 2u;
+        f8_group<C, FA, FB, true>(c, 0, acc, r, o);
+        for (int k0 = 8; k0 < c.steps; k0 += 8) f8_group<C, FA, FB, false>(c, k0, acc, r, o);
+        f8_store_private<C, BIAS>(acc, tm, tn, M, N, rC, ldc, wave, lane);
+        vb += P;
+        if (vb >= tiles) break;
+        tm = tm_next;
+        tn = tn_next;
+#pragma unroll
+        for (int v = 0; v < C::kLoads; ++v) c.row[v] = c.row_next[v];
+#pragma unroll
+        for (int v = 0; v < C::kScaleLoads; ++v) c.sc[v] = c.sc_next[v];
+        c.parity ^= c.kgroups & 1;
+        look_ahead();
+    }
+    // drain the stores and the trailing (out-of-range) DMAs
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 // ------------------------------------------------------------ few rows
@@ -441,6 +636,15 @@ hipError_t launch_formats(const F8GemmArgs &a, hipStream_t stream) {
             auto kernel = gemm_f8_b128_kernel<F8Small, FA, FB, OUT_BF16>;
             hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles_m * tiles_n)), dim3(F8Small::kThreads), 0, stream, a.M,
                                a.N, K_pad, tiles_m, tiles_n, 8, a.A, a.As, a.B, a.Bs, a.bias, a.C, a.ldc);
+            break;
+        }
+        case F8Form::kPersistent: {
+            const int tiles_m = (int)cdiv(a.M, 256), tiles_n = (int)cdiv(a.N, 256);
+            if constexpr (OUT_BF16)
+                hipLaunchKernelGGL(a.bias ? (gemm_f8_b128_stream_kernel<F8Main, FA, FB, true>)
+                                          : (gemm_f8_b128_stream_kernel<F8Main, FA, FB, false>),
+                                   dim3((unsigned)device_cu_count()), dim3(F8Main::kThreads), 0, stream, (int)a.M,
+                                   (int)a.N, (int)K_pad, tiles_m, tiles_n, tiles_m <= 16 ? 4 : 8, a.A, a.As, a.B, a.Bs, a.bias, a.C, (int)a.ldc);
             break;
         }
         case F8Form::kTiles256: {

@@ -9,6 +9,7 @@ namespace mx {
 enum class F8Form {
     kFewRows,    // operands straight from memory to registers
     kTiles128,   // one 128x128 tile per workgroup
+    kPersistent, // one workgroup per CU, 256x256 tiles
     kTiles256    // one 256x256 tile per workgroup
 };
 
@@ -16,6 +17,9 @@ inline F8Form f8_gemm_form(const F8GemmArgs &a, int cus) {
     const auto tiles = [&](int bm, int bn) { return cdiv(a.M, bm) * cdiv(a.N, bn); };
     if (a.M <= 64 || 10 * tiles(64, 32) <= 26 * (int64_t)cus) return F8Form::kFewRows;
     if (10 * tiles(128, 128) <= 13 * (int64_t)cus) return F8Form::kTiles128;
+    if (cus > 0 && a.out_dtype == MX_BF16 && a.N % 8 == 0 && tiles(256, 256) > cus &&
+        a.M * a.ldc * 2 < (int64_t(1) << 31))
+        return F8Form::kPersistent;
     return F8Form::kTiles256;
 }
 

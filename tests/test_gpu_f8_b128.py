@@ -178,8 +178,8 @@ PRODUCTS = [
     (200, 100, 300), (1, 700, 5000),
     # 128 x 128 tiles
     (1500, 1500, 200), (1153, 1985, 1300), (2000, 1111, 520),
-    # 256 x 256 tiles
-    (2300, 2500, 600), (2304, 2560, 1024),
+    # 256 x 256 tiles, persistent where N is a multiple of 8 and the tiles outnumber the CUs
+    (2300, 2500, 600), (2304, 2560, 1024), (4000, 4300, 1100), (4360, 4104, 300), (8200, 4616, 513), (6000, 3601, 700),
 ]
 
 
