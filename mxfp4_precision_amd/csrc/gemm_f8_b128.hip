@@ -616,6 +616,10 @@ __global__ void f8_fill_kernel(T *Cout, int64_t M, int64_t N, int64_t ldc, const
     }
 }
 
+// Tile rows per band of the tile order: 4 and 8 within 1% but for 8192 x 4096 x
+// 1024 (37.8 us and 41.3), 16 up to 4% slower.
+constexpr int kBandRows = 4;
+
 template <int FA, int FB, bool OUT_BF16>
 hipError_t launch_formats(const F8GemmArgs &a, hipStream_t stream) {
     const int64_t K_pad = padded(a.K);
@@ -635,7 +639,7 @@ hipError_t launch_formats(const F8GemmArgs &a, hipStream_t stream) {
             const int tiles_m = (int)cdiv(a.M, 128), tiles_n = (int)cdiv(a.N, 128);
             auto kernel = gemm_f8_b128_kernel<F8Small, FA, FB, OUT_BF16>;
             hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles_m * tiles_n)), dim3(F8Small::kThreads), 0, stream, a.M,
-                               a.N, K_pad, tiles_m, tiles_n, 8, a.A, a.As, a.B, a.Bs, a.bias, a.C, a.ldc);
+                               a.N, K_pad, tiles_m, tiles_n, kBandRows, a.A, a.As, a.B, a.Bs, a.bias, a.C, a.ldc);
             break;
         }
         case F8Form::kPersistent: {
@@ -644,14 +648,14 @@ hipError_t launch_formats(const F8GemmArgs &a, hipStream_t stream) {
                 hipLaunchKernelGGL(a.bias ? (gemm_f8_b128_stream_kernel<F8Main, FA, FB, true>)
                                           : (gemm_f8_b128_stream_kernel<F8Main, FA, FB, false>),
                                    dim3((unsigned)device_cu_count()), dim3(F8Main::kThreads), 0, stream, (int)a.M,
-                                   (int)a.N, (int)K_pad, tiles_m, tiles_n, tiles_m <= 16 ? 4 : 8, a.A, a.As, a.B, a.Bs, a.bias, a.C, (int)a.ldc);
+                                   (int)a.N, (int)K_pad, tiles_m, tiles_n, kBandRows, a.A, a.As, a.B, a.Bs, a.bias, a.C, (int)a.ldc);
             break;
         }
         case F8Form::kTiles256: {
             const int tiles_m = (int)cdiv(a.M, 256), tiles_n = (int)cdiv(a.N, 256);
             auto kernel = gemm_f8_b128_kernel<F8Main, FA, FB, OUT_BF16>;
             hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles_m * tiles_n)), dim3(F8Main::kThreads), 0, stream, a.M,
-                               a.N, K_pad, tiles_m, tiles_n, tiles_m <= 16 ? 4 : 8, a.A, a.As, a.B, a.Bs, a.bias, a.C,
+                               a.N, K_pad, tiles_m, tiles_n, kBandRows, a.A, a.As, a.B, a.Bs, a.bias, a.C,
                                a.ldc);
             break;
         }

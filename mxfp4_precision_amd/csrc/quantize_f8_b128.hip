@@ -67,21 +67,31 @@ __device__ __forceinline__ uint32_t encode4(uint32_t w0, uint32_t w1, float scal
     return encode2<FMT, true>(encode2<FMT, false>(0u, w0, scale), w1, scale);
 }
 
-// 16 elements of row r from column j0: 0 outside the tensor.
+// 16 elements of row r from column j0: 0 outside the tensor.  A chunk of 8 in
+// which the row ends is read whole where another row follows (ldx is a multiple
+// of 8, so the chunk lies inside the row's stride) and by elements in the last
+// row, behind which the tensor may end; what is past N is masked.
 __device__ __forceinline__ void load16(const uint16_t *__restrict__ x, int64_t M, int64_t N, int64_t ldx, int64_t r,
                                        int64_t j0, u4_t (&v)[2]) {
     v[0] = v[1] = u4_t{};
-    if (r >= M || j0 >= N) return;
+    if (r >= M) return;
     const uint16_t *p = x + r * ldx + j0;
-    if (j0 + 16 <= N) {
-        v[0] = *reinterpret_cast<const u4_t *>(p);
-        v[1] = *reinterpret_cast<const u4_t *>(p + 8);
-    } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const uint32_t b = j0 + e < N ? p[e] : 0u;
-            v[e >> 3][(e & 7) >> 1] |= b << (16 * (e & 1));
+    for (int h = 0; h < 2; ++h) {
+        const int64_t left = N - (j0 + 8 * h);   // elements from here to the row's end
+        if (left >= 8 || (left > 0 && r + 1 < M)) {
+            v[h] = *reinterpret_cast<const u4_t *>(p + 8 * h);
+        } else if (left > 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {   // (all loads at once: past the end the last element again)
+                const uint32_t b = p[8 * h + (e < left ? e : (int)left - 1)];
+                v[h][e >> 1] |= b << (16 * (e & 1));
+            }
         }
+        if (left < 8)
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                v[h][w] &= (2 * w < left ? 0x0000FFFFu : 0u) | (2 * w + 1 < left ? 0xFFFF0000u : 0u);
     }
 }
 
@@ -102,7 +112,9 @@ __device__ __forceinline__ void store_scale(uint8_t *s, int64_t r, int64_t kb, i
         uint8_t *word = s + ((r >> 4) * cdiv(nb, 4) + (kb >> 2)) * 64 + (r & 15) * 4;
         word[kb & 3] = (uint8_t)c;
         if (kb == nb - 1)
-            for (int64_t e = (kb & 3) + 1; e < 4; ++e) word[e] = 0;
+#pragma unroll
+            for (int e = 1; e < 4; ++e)
+                if (e > (int)(kb & 3)) word[e] = 0;
     } else {
         s[r * nb + kb] = (uint8_t)c;
     }
@@ -110,18 +122,28 @@ __device__ __forceinline__ void store_scale(uint8_t *s, int64_t r, int64_t kb, i
 
 // FR, FC: formats of the row-wise and the column-wise blob, or -1: not wanted.
 template <int LAYOUT, int FR, int FC>
-__global__ __launch_bounds__(256) void quantize_f8_b128_kernel(F8QuantArgs a, int64_t tiles_n) {
+__global__ __launch_bounds__(256) void quantize_f8_b128_kernel(F8QuantArgs a, uint32_t tiles_n) {
     __shared__ u4_t s_code[FR >= 0 && FC >= 0 ? 2 : 1][1024];   // 128 blob rows x 8 chunks of 16 codes
-    __shared__ uint32_t s_col[4][64];                               // a wave's column maxima, two a word
+    __shared__ uint32_t s_col[4][64];        // a wave's column maxima, two a word
+    __shared__ __attribute__((aligned(16))) uint8_t s_scale[2][kTile];    // scale bytes of the tile's rows and columns
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int tr = t >> 3, tc = t & 7;
-    const int64_t tm = blockIdx.x / tiles_n, tn = blockIdx.x % tiles_n;
-    const int64_t r0 = tm * kTile, c0 = tn * kTile;
+    const uint32_t tm = blockIdx.x / tiles_n, tn = blockIdx.x - tm * tiles_n;
+    const int64_t r0 = (int64_t)tm * kTile, c0 = (int64_t)tn * kTile;
     const bool need_tile = (FR >= 0 && a.row_2d) || FC >= 0;
 
     u4_t v[4][2];
+    if (r0 + kTile <= a.M && c0 + kTile <= a.N) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load16(a.x, a.M, a.N, a.ldx, r0 + 4 * tr + i, c0 + 16 * tc, v[i]);
+        for (int i = 0; i < 4; ++i) {
+            const u4_t *p = reinterpret_cast<const u4_t *>(a.x + (r0 + 4 * tr + i) * a.ldx + c0 + 16 * tc);
+            v[i][0] = p[0];
+            v[i][1] = p[1];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load16(a.x, a.M, a.N, a.ldx, r0 + 4 * tr + i, c0 + 16 * tc, v[i]);
+    }
 
     uint32_t row_max[4];
     uint32_t cm[8];
@@ -179,7 +201,7 @@ __global__ __launch_bounds__(256) void quantize_f8_b128_kernel(F8QuantArgs a, in
 
     // Row-wise: chunk tc of row r at 8 r + (tc ^ r % 8).
     if constexpr (FR >= 0) {
-        const int64_t R16 = LAYOUT == MX_LAYOUT_TILED ? cdiv(a.M, 16) * 16 : a.M, nb = cdiv(a.N, kTile);
+        uint32_t bytes = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = 4 * tr + i;
@@ -191,14 +213,14 @@ __global__ __launch_bounds__(256) void quantize_f8_b128_kernel(F8QuantArgs a, in
                 q[e] = encode4<FR>(v[i][e >> 1][(e & 1) * 2], v[i][e >> 1][(e & 1) * 2 + 1], scale);
             if (c == 0xFFu) q = u4_t{};
             s_code[0][8 * r + (tc ^ (r & 7))] = q;
-            // (rows past the tensor: zero bytes)
-            if (tc == 0 && r0 + r < R16) store_scale<LAYOUT>(a.s_row, r0 + r, tn, nb, r0 + r < a.M ? c : 0u);
+            bytes |= (r0 + r < a.M ? c : 0u) << (8 * i);   // rows past the tensor: zero bytes
         }
+        if (tc == 0) reinterpret_cast<uint32_t *>(s_scale[0])[tr] = bytes;
     }
     // Column-wise: of column j, rows 16 h .. 16 h + 15 are chunk h, at 8 j +
     // (h ^ j % 8 ^ j / 16); the thread's 4 rows are one word of it.
     if constexpr (FC >= 0) {
-        const int64_t R16 = LAYOUT == MX_LAYOUT_TILED ? cdiv(a.N, 16) * 16 : a.N, nb = cdiv(a.M, kTile);
+        u4_t bytes = {};
         uint32_t *words = reinterpret_cast<uint32_t *>(&s_code[FR >= 0 ? 1 : 0][0]);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -211,10 +233,22 @@ __global__ __launch_bounds__(256) void quantize_f8_b128_kernel(F8QuantArgs a, in
             uint32_t q = encode4<FC>(w01, w23, scale_of(c));
             if (c == 0xFFu) q = 0u;
             words[4 * (8 * j + ((tr >> 2) ^ (j & 7) ^ tc)) + (tr & 3)] = q;
-            if (tr == 0 && c0 + j < R16) store_scale<LAYOUT>(a.s_col, c0 + j, tm, nb, c0 + j < a.N ? c : 0u);
+            bytes[e >> 2] |= (c0 + j < a.N ? c : 0u) << (8 * (e & 3));
         }
+        if (tr == 0) reinterpret_cast<u4_t *>(s_scale[1])[tc] = bytes;
     }
     __syncthreads();
+    if constexpr (FR >= 0) {
+        const int64_t R16 = LAYOUT == MX_LAYOUT_TILED ? cdiv(a.M, 16) * 16 : a.M;
+        if (t < kTile && r0 + t < R16)
+            store_scale<LAYOUT>(a.s_row, r0 + t, tn, cdiv(a.N, kTile), s_scale[0][t]);
+    }
+    if constexpr (FC >= 0) {
+        const int64_t R16 = LAYOUT == MX_LAYOUT_TILED ? cdiv(a.N, 16) * 16 : a.N;
+        const int j = t & (kTile - 1);
+        if (t >= kTile && c0 + j < R16)
+            store_scale<LAYOUT>(a.s_col, c0 + j, tm, cdiv(a.M, kTile), s_scale[1][j]);
+    }
     // Each wave stores atoms: 16 rows x 4 chunks.
     const int ar = lane & 15, ac = lane >> 4;
 #pragma unroll
@@ -240,10 +274,10 @@ hipError_t launch_pair(const F8QuantArgs &a, mx_layout layout, hipStream_t strea
     const int64_t tiles_n = cdiv(a.N, kTile);
     const dim3 grid((unsigned)(tiles_n * cdiv(a.M, kTile)));
     if (layout == MX_LAYOUT_TILED)
-        hipLaunchKernelGGL((quantize_f8_b128_kernel<MX_LAYOUT_TILED, FR, FC>), grid, dim3(256), 0, stream, a, tiles_n);
+        hipLaunchKernelGGL((quantize_f8_b128_kernel<MX_LAYOUT_TILED, FR, FC>), grid, dim3(256), 0, stream, a, (uint32_t)tiles_n);
     else
         hipLaunchKernelGGL((quantize_f8_b128_kernel<MX_LAYOUT_CANONICAL, FR, FC>), grid, dim3(256), 0, stream, a,
-                           tiles_n);
+                           (uint32_t)tiles_n);
     return hipGetLastError();
 }
 
