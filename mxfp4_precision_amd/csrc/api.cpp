@@ -547,7 +547,7 @@ mx_status mx_linear_f8_b128_bytes(int64_t M, int64_t K, size_t *bytes) {
     size_t data, scale;
     MX_TRY(mx_f8_b128_blob_bytes(M, K, MX_LAYOUT_TILED, &data, &scale));
     if (!bytes) return fail(MX_ERR_INVALID_ARGUMENT, "bytes is NULL");
-    *bytes = data + scale;   // (data: whole kilobytes, so the scales are aligned)
+    *bytes = mx::f8_linear_fused(M) ? 0 : data + scale;   // (data: whole kilobytes, so the scales are aligned)
     return MX_SUCCESS;
 }
 
@@ -569,16 +569,12 @@ mx_status mx_linear_f8_b128(int64_t M, int64_t N, int64_t K, int fmt_x, const vo
     }
     if (M == 0 || N == 0) return MX_SUCCESS;
     MX_TRY(check_device());
-    uint8_t *q = static_cast<uint8_t *>(workspace);
-    const mx::F8GemmArgs g{M, N, K, fmt_x, fmt_w, q, q + data, static_cast<const uint8_t *>(W),
-                           static_cast<const uint8_t *>(W_scale), static_cast<const uint16_t *>(bias), out_dtype, y,
-                           ldy};
-    if (K > 0) {
-        const mx::F8QuantArgs a{static_cast<const uint16_t *>(x), M, K, ldx, fmt_x, 0, false, false, q, q + data,
-                                nullptr, nullptr};
-        MX_TRY(check_launch(mx::launch_quantize_f8_b128(a, MX_LAYOUT_TILED, stream), name));
-    }
-    return check_launch(mx::launch_gemm_f8_b128(g, stream), name);
+    const uint8_t *q = static_cast<const uint8_t *>(workspace);
+    const mx::F8LinearArgs a{static_cast<const uint16_t *>(x), ldx,
+                             {M, N, K, fmt_x, fmt_w, q, q + data, static_cast<const uint8_t *>(W),
+                              static_cast<const uint8_t *>(W_scale), static_cast<const uint16_t *>(bias), out_dtype, y,
+                              ldy}};
+    return check_launch(mx::launch_linear_f8_b128(a, stream), name);
 }
 
 namespace {

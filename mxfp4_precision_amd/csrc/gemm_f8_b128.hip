@@ -22,6 +22,7 @@
 // k-step is kSlots slots of one MFMA, one or two operand reads of the next step
 // and the DMA instructions of the step three ahead, in fixed order.
 
+#include "f8_b128.h"
 #include "gemm_f8_b128_forms.h"
 #include "gemm_pipeline.h"
 
@@ -604,6 +605,101 @@ __global__ __launch_bounds__(256) void gemm_f8_b128_few_kernel(int64_t M, int64_
                                    lane);
 }
 
+// A linear layer on up to 16 rows in one launch: as the few-rows product, but a
+// wave quantizes the blocks of x that it multiplies.  Lane L holds row L % 16's
+// slice L / 16 of both halves of a block, so the block's maximum is a lane
+// exchange away and the codes are the operand; every workgroup does so for itself
+// (x is small and stays in the L2s), while its weights are on their way.
+template <int FX, int FW, int DEPTH>
+__device__ __forceinline__ void f8_linear_sum(const uint16_t *__restrict__ x, int64_t M, int64_t K, int64_t ldx,
+                                              __amdgpu_buffer_rsrc_t rB, __amdgpu_buffer_rsrc_t rBs, int g,
+                                              int kblocks, int kgroups, int wave, int lane, v4f &acc, int h0 = 0) {
+    const uint32_t lane16 = (uint32_t)lane * 16, word = (uint32_t)(lane & 15) * 4;
+    const int64_t r = lane & 15;
+    for (; h0 + DEPTH <= kgroups; h0 += DEPTH) {
+        v4u_t b[DEPTH][2];
+        uint32_t bs[DEPTH];
+        u4_t v[DEPTH][4];
+#pragma unroll
+        for (int u = 0; u < DEPTH; ++u) {
+            const int h = h0 + u, kb = 4 * h + wave;
+            const bool in = kb < kblocks;   // past K: zeros (see f8_dma)
+            const uint32_t off = in ? lane16 : kOutOfRange;
+            const int at = in ? (g * kblocks + kb) * 2048 : 0;
+            b[u][0] = __builtin_amdgcn_raw_buffer_load_b128(rB, off, at, 0);
+            b[u][1] = __builtin_amdgcn_raw_buffer_load_b128(rB, off + 1024, at, 0);
+            bs[u] = __builtin_amdgcn_raw_buffer_load_b32(rBs, word, (g * kgroups + h) * 64, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < DEPTH; ++u) {
+            const int64_t k0 = 128 * (int64_t)(4 * (h0 + u) + wave), k = k0 + 16 * (lane >> 4);
+            if (k0 + 128 <= K) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) v[u][w] = u4_t{};
+                if (r < M) {
+                    const u4_t *p = reinterpret_cast<const u4_t *>(x + r * ldx + k);
+                    v[u][0] = p[0]; v[u][1] = p[1]; v[u][2] = p[8]; v[u][3] = p[9];
+                }
+            } else {
+                u4_t lo[2], hi[2];
+                load16(x, M, K, ldx, r, k, lo);
+                load16(x, M, K, ldx, r, k + 64, hi);
+                v[u][0] = lo[0]; v[u][1] = lo[1]; v[u][2] = hi[0]; v[u][3] = hi[1];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < DEPTH; ++u) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int w = 0; w < 16; ++w) m = max2(m, v[u][w >> 2][w & 3] & 0x7FFF7FFFu);
+            m = max2_xor(m, 16);
+            m = max2_xor(m, 32);
+            const uint32_t c = scale_byte<FX>((m & 0xFFFFu) > (m >> 16) ? (m & 0xFFFFu) : (m >> 16));
+            const float scale = scale_of(c);
+            v8i aop;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                const uint32_t q = encode4<FX>(v[u][w >> 1][(w & 1) * 2], v[u][w >> 1][(w & 1) * 2 + 1], scale);
+                aop[w] = c == 0xFFu ? 0 : (int)q;
+            }
+            const v8i bop = {(int)b[u][0][0], (int)b[u][0][1], (int)b[u][0][2], (int)b[u][0][3],
+                             (int)b[u][1][0], (int)b[u][1][1], (int)b[u][1][2], (int)b[u][1][3]};
+            const int sb = (int)(bs[u] >> (8 * wave)), sa = (int)c;
+            const v4f cin = acc;
+            acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bop, aop, cin, FW, FX, 0, sb, 0, sa);
+        }
+    }
+    if constexpr (DEPTH > 1)
+        f8_linear_sum<FX, FW, DEPTH / 2>(x, M, K, ldx, rB, rBs, g, kblocks, kgroups, wave, lane, acc, h0);
+}
+
+template <int FX, int FW, bool OUT_BF16>
+__global__ __launch_bounds__(256) void linear_f8_b128_kernel(int64_t M, int64_t N, int64_t K,
+                                                             const uint16_t *__restrict__ x, int64_t ldx,
+                                                             const uint8_t *__restrict__ W,
+                                                             const uint8_t *__restrict__ Ws,
+                                                             const uint16_t *__restrict__ bias, void *__restrict__ y,
+                                                             int64_t ldy) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kblocks = (int)cdiv(K, 128), kgroups = (kblocks + 3) / 4, nGB = (int)cdiv(N, 16);
+    const int gB0 = (int)blockIdx.x;
+    v4f acc[1][1] = {};
+    f8_linear_sum<FX, FW, 4>(x, M, K, ldx, make_rsrc(W, (int64_t)nGB * kblocks * 2048),
+                             make_rsrc(Ws, (int64_t)nGB * kgroups * 64), gB0, kblocks, kgroups, wave, lane, acc[0][0]);
+    f8_few_store<1, 1, OUT_BF16>(acc, 0, 16 * (int64_t)gB0, M, N, bias, y, ldy, wave, lane);
+}
+
+template <int FX, int FW>
+hipError_t launch_linear(const F8LinearArgs &a, hipStream_t stream) {
+    const F8GemmArgs &g = a.g;
+    const bool bf = g.out_dtype == MX_BF16;
+    auto kernel = bf ? linear_f8_b128_kernel<FX, FW, true> : linear_f8_b128_kernel<FX, FW, false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)cdiv(g.N, 16)), dim3(256), 0, stream, g.M, g.N, g.K, a.x, a.ldx, g.B,
+                       g.Bs, g.bias, g.C, g.ldc);
+    return hipGetLastError();
+}
+
 // K == 0: C[i][j] = 0, or bias[j].
 template <typename T>
 __global__ void f8_fill_kernel(T *Cout, int64_t M, int64_t N, int64_t ldc, const uint16_t *bias) {
@@ -685,6 +781,22 @@ hipError_t launch_gemm_f8_b128(const F8GemmArgs &a, hipStream_t stream) {
     if (a.fmt_a == MX_FP8_E4M3)
         return a.fmt_b == MX_FP8_E4M3 ? launch_out<0, 0>(a, stream) : launch_out<0, 1>(a, stream);
     return a.fmt_b == MX_FP8_E4M3 ? launch_out<1, 0>(a, stream) : launch_out<1, 1>(a, stream);
+}
+
+hipError_t launch_linear_f8_b128(const F8LinearArgs &a, hipStream_t stream) {
+    if (a.g.K > 0 && f8_linear_fused(a.g.M)) {
+        if (a.g.fmt_a == MX_FP8_E4M3)
+            return a.g.fmt_b == MX_FP8_E4M3 ? launch_linear<0, 0>(a, stream) : launch_linear<0, 1>(a, stream);
+        return a.g.fmt_b == MX_FP8_E4M3 ? launch_linear<1, 0>(a, stream) : launch_linear<1, 1>(a, stream);
+    }
+    if (a.g.K > 0) {
+        // (the workspace is the blob of x)
+        const F8QuantArgs q{a.x, a.g.M, a.g.K, a.ldx, a.g.fmt_a, 0, false, false, const_cast<uint8_t *>(a.g.A),
+                            const_cast<uint8_t *>(a.g.As), nullptr, nullptr};
+        const hipError_t e = launch_quantize_f8_b128(q, MX_LAYOUT_TILED, stream);
+        if (e != hipSuccess) return e;
+    }
+    return launch_gemm_f8_b128(a.g, stream);
 }
 
 }  // namespace mx

@@ -127,6 +127,7 @@ hipError_t launch_quantize_fp8(const uint16_t *x, int64_t M, int64_t N, int64_t 
                                uint8_t *q_row, uint8_t *q_col, float *info, hipStream_t stream);
 hipError_t launch_quantize_f8_b128(const F8QuantArgs &a, mx_layout layout, hipStream_t stream);
 hipError_t launch_gemm_f8_b128(const F8GemmArgs &a, hipStream_t stream);
+hipError_t launch_linear_f8_b128(const F8LinearArgs &a, hipStream_t stream);
 hipError_t launch_layout_convert(bool to_tiled, int64_t rows, int64_t length, const uint8_t *q_src,
                                  const uint8_t *s_src, uint8_t *q_dst, uint8_t *s_dst, hipStream_t stream);
 hipError_t launch_quantize_grouped(const QuantArgs &a, bool dual, hipStream_t stream);

@@ -193,3 +193,58 @@ def test_product(shape):
     if small:
         for fa, fb in ((0, 0), (1, 0), (0, 1), (1, 1)):
             check_product(M, N, K, fa, fb, codes_of, what="codes %d %d" % (fa, fb))
+
+
+# ------------------------------------------------------------------ a linear layer in one call
+@pytest.mark.parametrize("fx,fw", [(0, 0), (1, 0), (0, 1), (1, 1)])
+@pytest.mark.parametrize("M", [1, 5, 16, 17, 64, 700])
+def test_linear(M, fx, fw):
+    """One launch or two, the product of x's codes; x lies in a wider buffer whose other columns hold NaN, and its last
+    row ends where the tensor ends."""
+    for N, K in ((40, 128), (33, 1000), (256, 2049), (1, 1), (65, 520)):
+        rng = np.random.default_rng(M + N)
+        bits = synth.normal(rng, (M, K), 1.0).reshape(M, K)
+        bits[:, K // 2] = 0
+        bits[M // 2] &= 0x81FF                                         # a row of tiny values
+        ldx = (K + 7) // 8 * 8 + 8
+        flat = np.full((M - 1) * ldx + K, 0x7FC0, np.uint16)
+        for r in range(M):
+            flat[r * ldx:r * ldx + K] = bits[r]
+        x = torch.from_numpy(flat.view(np.int16)).cuda()
+        w = normal_codes(N, K, fw, 7)
+        a = ref.quantize(bits, 0, fx)
+        want = ref.product(a, w, fx, fw)
+        bb = synth.normal(rng, (N,), 1.0).reshape(-1)
+        bias = torch.zeros(-(-N // 8) * 8, dtype=torch.int16)
+        bias[:N] = torch.from_numpy(bb.view(np.int16))
+        bias = bias.cuda()
+        ws = torch.full((mx.mx_linear_f8_b128_bytes(M, K) + 16,), 0xA5, dtype=torch.uint8, device="cuda")
+        ldy = (N + 7) // 8 * 8 + 8
+        for dt, add in ((mx.MX_F32, None), (mx.MX_F32, bias), (mx.MX_BF16, bias)):
+            y = torch.full((M + 1, ldy), -7.0, dtype=torch.float32 if dt == mx.MX_F32 else torch.bfloat16, device="cuda")
+            mx.mx_linear_f8_b128(M, N, K, fx, x, ldx, fw, *dev_blob(*w), T, dt, add, y, ldy, ws)
+            got = y.double().cpu().numpy()
+            assert (got[M:] == -7).all() and (got[:, N:] == -7).all(), "written outside y"
+            if dt == mx.MX_F32:
+                check_entries(got[:M, :N], *want, None if add is None else ref.to_f64(bb), "linear %d" % K)
+                last = y
+            else:
+                assert torch.equal(y[:M, :N], last[:M, :N].bfloat16())
+        assert (ws[-16:] == 0xA5).all()
+
+
+def test_linear_with_non_finite_rows():
+    """NaN where a block of the row holds Inf or NaN, the other rows as ever."""
+    for M in (3, 50):
+        bits = synth.normal(np.random.default_rng(0), (M, 300), 1.0).reshape(M, 300)
+        bits[1, 200], bits[2, 3] = 0x7F80, 0x7FFF
+        w = normal_codes(40, 300, 0, 1)
+        y = torch.empty(M, 40, dtype=torch.float32, device="cuda")
+        ws = torch.empty(mx.mx_linear_f8_b128_bytes(M, 300) + 1, dtype=torch.uint8, device="cuda")
+        x, ldx = to_dev_bf16(bits)
+        mx.mx_linear_f8_b128(M, 40, 300, 0, x, ldx, 0, *dev_blob(*w), T, mx.MX_F32, None, y, 40, ws)
+        got = y.double().cpu().numpy()
+        assert np.isnan(got[1:3]).all() and np.isfinite(np.delete(got, (1, 2), 0)).all()
+        keep = np.delete(np.arange(M), (1, 2))
+        want = ref.product([v[keep] for v in ref.quantize(bits, 0, 0)], w, 0, 0)
+        check_entries(got[keep], *want)
