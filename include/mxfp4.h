@@ -551,6 +551,66 @@ mx_status mx_adamw_step_values(const mx_adamw_opts *opts, mx_adamw_step *step);
  */
 mx_status mx_adamw(const mx_adamw_tensor *tensors, int64_t count, const mx_adamw_opts *opts, hipStream_t stream);
 
+/*
+ * ---- The gradients' norm, and clipping ----
+ * sum_sq: the sum of the squares of all elements of all tensors, in 64 bits and
+ * in a fixed order.  With grad_scale (1 / loss scale):
+ *   norm = grad_scale * sqrt(sum_sq)
+ *   scale = grad_scale * min(1, max_norm / (norm + 1e-6))
+ * scale is mx_adamw's grad_scale: a training step takes it by device_step and
+ * the gradients need not be written again, or mx_clip_grads multiplies them.  A
+ * norm of Inf gives scale 0 (Inf gradients then become NaN), a NaN one NaN:
+ * finite norms are the caller's check.  max_norm = infinity clips nothing:
+ * scale is grad_scale, whatever the norm.
+ */
+typedef struct mx_grad_tensor {
+    void *grad;            /* numel of dtype */
+    int64_t numel;
+    int dtype;             /* MX_F32 or MX_BF16 */
+} mx_grad_tensor;
+
+/* In device memory; 8-byte aligned. */
+typedef struct mx_grad_norm_info {
+    double sum_sq;
+    float norm;
+    float scale;
+} mx_grad_norm_info;
+
+/* Workspace of mx_grad_norm for `count` tensors of any size.
+ * Errors: MX_ERR_INVALID_ARGUMENT (count < 0). */
+mx_status mx_grad_norm_bytes(int64_t count, size_t *bytes);
+
+/*
+ * Norm and scale of tensors[0..count) (a host array, read before the call
+ * returns) into info.  step: NULL, or a device mx_adamw_step whose grad_scale
+ * becomes the scale (its other fields stay).  max_norm: >= 0, infinity for the
+ * norm alone.  Tensors with numel == 0 are skipped; without elements the norm
+ * is 0.  workspace: mx_grad_norm_bytes(count) bytes, 8-byte aligned; calls that
+ * share it, or info, must not overlap.
+ * Requires gradients 16-byte aligned.
+ * Errors: MX_ERR_INVALID_ARGUMENT (NULL, count < 0, numel < 0, max_norm < 0 or
+ * NaN, grad_scale < 0 or not finite in fp32), MX_ERR_MISALIGNED, MX_ERR_UNSUPPORTED (a dtype,
+ * numel above 2^33, count above 2^20), MX_ERR_DEVICE_UNSUPPORTED, MX_ERR_HIP.
+ */
+mx_status mx_grad_norm(const mx_grad_tensor *tensors, int64_t count, double max_norm, double grad_scale,
+                       void *workspace, mx_grad_norm_info *info, mx_adamw_step *step, hipStream_t stream);
+
+/*
+ * Norm and scale again from info's sum_sq, for gradients that are spread over
+ * processes: mx_grad_norm on each one's part, sum_sq added up over them, then
+ * this.  Errors as mx_grad_norm.
+ */
+mx_status mx_grad_norm_finish(double max_norm, double grad_scale, mx_grad_norm_info *info, mx_adamw_step *step,
+                              hipStream_t stream);
+
+/*
+ * Every gradient times info's scale, in place: the product in fp32, rounded to
+ * nearest even where the gradient is bf16.  No two tensors may overlap.
+ * Requirements and errors as mx_grad_norm.
+ */
+mx_status mx_clip_grads(const mx_grad_tensor *tensors, int64_t count, const mx_grad_norm_info *info,
+                        hipStream_t stream);
+
 /* ------------------------------------------------------------------ MXFP6
  *
  * MXFP6: the same 32-element blocks and E8M0 scales with 6-bit elements.

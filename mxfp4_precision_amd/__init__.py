@@ -46,7 +46,7 @@ EXPORTED = ("mx_blob_bytes", "mx_quantize_rowwise", "mx_quantize_dual", "mx_gemm
             "mx_grouped_blob_bytes", "mx_quantize_grouped", "mx_gemm_a4w4_grouped", "mx_gemm_a4w4_grouped_wgrad",
             "mx_adamw", "mx_adamw_step_values",
             "mx_f8_b128_blob_bytes", "mx_quantize_fp8_b128", "mx_gemm_f8_b128", "mx_linear_f8_b128_bytes",
-            "mx_linear_f8_b128",
+            "mx_linear_f8_b128", "mx_grad_norm_bytes", "mx_grad_norm", "mx_grad_norm_finish", "mx_clip_grads",
             "mx_measure_mfma", "mx_set_device_arch_override", "mx_status_string", "mx_last_error")
 
 
@@ -108,6 +108,20 @@ def adamw_table(rows):
     return (mx_adamw_tensor * max(len(rows), 1))(*rows)
 
 
+class mx_grad_tensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+def grad_tensor(grad, numel: int, dtype: int) -> mx_grad_tensor:
+    """One row of a table of gradients.  It holds an address: the caller keeps the tensor alive."""
+    return mx_grad_tensor(_dptr(grad), numel, dtype)
+
+
+def grad_table(rows):
+    """The host array of mx_grad_norm and mx_clip_grads (built once, used every step while the addresses stay)."""
+    return (mx_grad_tensor * max(len(rows), 1))(*rows)
+
+
 try:
     from . import _marshal      # converts the arguments of the grouped calls (csrc/marshal.cpp)
 except ImportError:
@@ -153,6 +167,11 @@ def lib() -> ctypes.CDLL:
     L.mx_gemm_f8_b128.argtypes = [i32, i32, i64, i64, i64, i32, vp, vp, i32, vp, vp, i32, i32, vp, vp, i64, vp]
     L.mx_linear_f8_b128_bytes.argtypes = [i64, i64, szp]
     L.mx_linear_f8_b128.argtypes = [i64, i64, i64, i32, vp, i64, i32, vp, vp, i32, i32, vp, vp, i64, vp, vp]
+    gradp, f64 = ctypes.POINTER(mx_grad_tensor), ctypes.c_double
+    L.mx_grad_norm_bytes.argtypes = [i64, szp]
+    L.mx_grad_norm.argtypes = [gradp, i64, f64, f64, vp, vp, vp, vp]
+    L.mx_grad_norm_finish.argtypes = [f64, f64, vp, vp, vp]
+    L.mx_clip_grads.argtypes = [gradp, i64, vp, vp]
     L.mx_dequantize.argtypes = [vp, vp, i64, i64, i32, vp, i64, vp]
     L.mx_measure_mfma.argtypes = [i32, i32, vp, i32, i64, vp, vp]
     L.mx_set_device_arch_override.argtypes = [ctypes.c_char_p]
@@ -414,6 +433,35 @@ def mx_adamw_step_values(opts: mx_adamw_opts) -> mx_adamw_step:
     step = mx_adamw_step()
     _check(lib().mx_adamw_step_values(ctypes.byref(opts), ctypes.byref(step)))
     return step
+
+
+def mx_grad_norm_bytes(count: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().mx_grad_norm_bytes(count, ctypes.byref(n)))
+    return n.value
+
+
+def _table(tensors, count: int):
+    if tensors is not None and count > len(tensors):
+        raise ValueError("count=%d, but the table holds %d tensors" % (count, len(tensors)))
+    return tensors
+
+
+def mx_grad_norm(tensors, count: int, max_norm: float, grad_scale: float, workspace, info, step=None, stream=None):
+    """tensors: an array of grad_table.  info: a GPU tensor that holds an mx_grad_norm_info (16 bytes: the sum of
+    squares as a float64, norm and scale as float32); step: one that holds an mx_adamw_step, or None.  workspace: a
+    tensor or pointer of mx_grad_norm_bytes(count) bytes; a shorter tensor is refused."""
+    _room(workspace, mx_grad_norm_bytes, count)
+    _check(lib().mx_grad_norm(_table(tensors, count), count, max_norm, grad_scale, _dptr(workspace), _dptr(info),
+                              _dptr(step), _stream(stream)))
+
+
+def mx_grad_norm_finish(max_norm: float, grad_scale: float, info, step=None, stream=None):
+    _check(lib().mx_grad_norm_finish(max_norm, grad_scale, _dptr(info), _dptr(step), _stream(stream)))
+
+
+def mx_clip_grads(tensors, count: int, info, stream=None):
+    _check(lib().mx_clip_grads(_table(tensors, count), count, _dptr(info), _stream(stream)))
 
 
 def mx_layout_convert(to_tiled: int, rows: int, length: int, q_src, s_src, q_dst, s_dst, stream=None):

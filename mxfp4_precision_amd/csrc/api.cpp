@@ -139,6 +139,35 @@ mx_status check_blob_limit(const char *name, const char *which, int64_t rows, in
         if (_st != MX_SUCCESS) return _st; \
     } while (0)
 
+// Chunks of one launch: a grid of 256-thread workgroups must stay below 2^32 threads.
+constexpr int64_t kMaxChunks = int64_t(1) << 23;
+
+// Calls launch(batch) for the tensors in tables of kGradItems items and at most
+// kMaxChunks chunks of `chunk` elements.
+template <typename F>
+mx_status grad_tables(const mx_grad_tensor *tensors, int64_t count, int64_t chunk, F launch) {
+    mx::GradBatch b;   // entries past its count are never read
+    b.chunk = chunk;
+    b.count = 0;
+    int64_t chunks = 0;
+    const auto flush = [&]() -> mx_status {
+        if (b.count == 0) return MX_SUCCESS;
+        const mx_status st = launch(b);
+        b.count = 0;
+        chunks = 0;
+        return st;
+    };
+    for (int64_t i = 0; i < count; ++i) {
+        const mx_grad_tensor &t = tensors[i];
+        if (t.numel == 0) continue;
+        const int64_t n = mx::cdiv(t.numel, chunk);
+        if (b.count == mx::kGradItems || chunks + n > kMaxChunks) MX_TRY(flush());
+        chunks += n;
+        b.t[b.count++] = mx::GradItem{t.grad, t.numel, (uint32_t)chunks, t.dtype == MX_F32 ? 1u : 0u};
+    }
+    return flush();
+}
+
 }  // namespace
 
 extern "C" {
@@ -751,9 +780,6 @@ mx_status check_adamw_opts(const mx_adamw_opts *o) {
 
 bool float_dtype(int t) { return t == MX_F32 || t == MX_BF16; }
 
-// Chunks of one launch: a grid of 256-thread workgroups must stay below 2^32 threads.
-constexpr int64_t kMaxChunks = int64_t(1) << 23;
-
 }  // namespace
 
 mx_status mx_adamw_step_values(const mx_adamw_opts *opts, mx_adamw_step *step) {
@@ -824,6 +850,97 @@ mx_status mx_adamw(const mx_adamw_tensor *tensors, int64_t count, const mx_adamw
                                        (uint32_t)chunks, t.tensor_id};
     }
     return flush();
+}
+
+namespace {
+
+mx_status check_grads(const mx_grad_tensor *tensors, int64_t count) {
+    if (count < 0 || (count > 0 && !tensors)) return fail(MX_ERR_INVALID_ARGUMENT, "tensors is NULL or count negative");
+    if (count > (int64_t(1) << 20)) return fail(MX_ERR_UNSUPPORTED, "count=%lld is above 2^20", (long long)count);
+    for (int64_t i = 0; i < count; ++i) {
+        const mx_grad_tensor &t = tensors[i];
+        if (t.numel < 0) return fail(MX_ERR_INVALID_ARGUMENT, "tensor %lld: negative numel", (long long)i);
+        if (!float_dtype(t.dtype))
+            return fail(MX_ERR_UNSUPPORTED, "tensor %lld: dtype %d (valid: MX_BF16=0, MX_F32=1)", (long long)i, t.dtype);
+        if (t.numel > (int64_t(1) << 33))
+            return fail(MX_ERR_UNSUPPORTED, "tensor %lld: numel=%lld is above 2^33", (long long)i, (long long)t.numel);
+        if (t.numel == 0) continue;
+        if (!t.grad) return fail(MX_ERR_INVALID_ARGUMENT, "tensor %lld: NULL pointer", (long long)i);
+        if (!aligned16(t.grad)) return fail(MX_ERR_MISALIGNED, "tensor %lld: grad must be 16-byte aligned", (long long)i);
+    }
+    return MX_SUCCESS;
+}
+
+bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+mx_status check_grad_norm(double max_norm, double grad_scale, const mx_grad_norm_info *info, const mx_adamw_step *step) {
+    if (!(max_norm >= 0)) return fail(MX_ERR_INVALID_ARGUMENT, "max_norm=%g must be >= 0", max_norm);
+    if (!(grad_scale >= 0) || !std::isfinite((float)grad_scale))
+        return fail(MX_ERR_INVALID_ARGUMENT, "grad_scale=%g must be >= 0 and finite in fp32", grad_scale);
+    if (!info) return fail(MX_ERR_INVALID_ARGUMENT, "info is NULL");
+    if (!aligned8(info) || !aligned8(step)) return fail(MX_ERR_MISALIGNED, "info and step must be 8-byte aligned");
+    return MX_SUCCESS;
+}
+
+}  // namespace
+
+mx_status mx_grad_norm_bytes(int64_t count, size_t *bytes) {
+    if (count < 0) return fail(MX_ERR_INVALID_ARGUMENT, "count negative");
+    if (!bytes) return fail(MX_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    if (count > (int64_t(1) << 20)) return fail(MX_ERR_UNSUPPORTED, "count=%lld is above 2^20", (long long)count);
+    *bytes = (size_t)(mx::kGradChunks + count) * sizeof(double);
+    return MX_SUCCESS;
+}
+
+mx_status mx_grad_norm(const mx_grad_tensor *tensors, int64_t count, double max_norm, double grad_scale,
+                       void *workspace, mx_grad_norm_info *info, mx_adamw_step *step, hipStream_t stream) {
+    const char *name = "mx_grad_norm";
+    MX_TRY(check_grads(tensors, count));
+    MX_TRY(check_grad_norm(max_norm, grad_scale, info, step));
+    if (!workspace) return fail(MX_ERR_INVALID_ARGUMENT, "workspace is NULL");
+    if (!aligned8(workspace)) return fail(MX_ERR_MISALIGNED, "workspace must be 8-byte aligned");
+    MX_TRY(check_device());
+    const mx::GradNormOut o{max_norm, grad_scale, info, step};
+    int64_t total = 0, some = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        total += tensors[i].numel;   // (at most 2^53)
+        some += tensors[i].numel != 0;
+    }
+    if (some > 0 && some <= mx::kGradFew && total <= mx::kGradFewTotal)
+        return grad_tables(tensors, count, mx::kGradFewTotal, [&](const mx::GradBatch &b) {
+            return check_launch(mx::launch_grad_norm_few(b, o, stream), name);
+        });
+    const int64_t chunk = mx::grad_chunk(total);
+    double *sums = static_cast<double *>(workspace);
+    int n = 0;
+    MX_TRY(grad_tables(tensors, count, chunk, [&](const mx::GradBatch &b) {
+        const mx_status st = check_launch(mx::launch_grad_sums(b, sums + n, stream), name);
+        n += (int)b.t[b.count - 1].chunk_end;
+        return st;
+    }));
+    return check_launch(mx::launch_grad_norm(sums, n, o, stream), name);
+}
+
+mx_status mx_grad_norm_finish(double max_norm, double grad_scale, mx_grad_norm_info *info, mx_adamw_step *step,
+                              hipStream_t stream) {
+    MX_TRY(check_grad_norm(max_norm, grad_scale, info, step));
+    MX_TRY(check_device());
+    return check_launch(mx::launch_grad_finish(mx::GradNormOut{max_norm, grad_scale, info, step}, stream),
+                        "mx_grad_norm_finish");
+}
+
+mx_status mx_clip_grads(const mx_grad_tensor *tensors, int64_t count, const mx_grad_norm_info *info,
+                        hipStream_t stream) {
+    MX_TRY(check_grads(tensors, count));
+    if (!info) return fail(MX_ERR_INVALID_ARGUMENT, "info is NULL");
+    if (!aligned8(info)) return fail(MX_ERR_MISALIGNED, "info must be 8-byte aligned");
+    bool any = false;
+    for (int64_t i = 0; i < count; ++i) any |= tensors[i].numel != 0;
+    if (!any) return MX_SUCCESS;
+    MX_TRY(check_device());
+    return grad_tables(tensors, count, mx::kScaleChunk, [&](const mx::GradBatch &b) {
+        return check_launch(mx::launch_grad_scale(b, info, stream), "mx_clip_grads");
+    });
 }
 
 mx_status mx_layout_convert(int to_tiled, int64_t rows, int64_t length, const void *q_src, const void *s_src,

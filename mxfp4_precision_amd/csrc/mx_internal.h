@@ -104,6 +104,37 @@ struct AdamwTable {
 using AdamwBatch = AdamwTable<kAdamwItems>;
 static_assert(sizeof(AdamwBatch) <= 4000, "kernel arguments");
 
+// Gradients of one launch, passed as kernel arguments.
+struct GradItem {
+    void *g;
+    int64_t numel;
+    uint32_t chunk_end;         // workgroups of this and the items before it
+    uint32_t f32;               // 1: fp32, 0: bf16
+};
+constexpr int kGradItems = 96, kGradFew = 8;
+template <int ITEMS>
+struct GradTable {
+    int64_t chunk;              // elements of a workgroup, a multiple of 8
+    int count;
+    GradItem t[ITEMS];
+};
+using GradBatch = GradTable<kGradItems>;
+static_assert(sizeof(GradBatch) <= 4000, "kernel arguments");
+struct GradNormOut {
+    double max_norm, grad_scale;
+    mx_grad_norm_info *info;
+    mx_adamw_step *step;        // or NULL
+};
+// The norm's chunks: all tensors make kGradChunks of them at most, and one more
+// for each tensor.
+constexpr int64_t kGradChunks = 2048;
+inline int64_t grad_chunk(int64_t total) {
+    const int64_t even = cdiv(cdiv(total, kGradChunks), 8) * 8;
+    return even > 8192 ? even : 8192;
+}
+constexpr int64_t kScaleChunk = 8192;       // elements that a workgroup scales
+constexpr int64_t kGradFewTotal = 16384;    // elements of up to kGradFew tensors that one workgroup sums
+
 // Grid dimension y of one launch holds at most 65536 workgroups on gfx950
 // (hipDeviceAttributeMaxGridDimY); the quantize launchers cover taller inputs
 // with several launches of kMaxRowTiles row tiles each.
@@ -135,6 +166,11 @@ hipError_t launch_gemm_grouped(const GroupedGemmArgs &a, hipStream_t stream);
 hipError_t launch_gemm_grouped_wgrad(const GroupedGemmArgs &a, hipStream_t stream);
 int64_t adamw_chunks(int64_t numel);   // workgroups that numel elements take
 hipError_t launch_adamw(const AdamwBatch &b, bool p32, bool g32, bool s8, bool sr, hipStream_t stream);
+hipError_t launch_grad_sums(const GradBatch &b, double *sums, hipStream_t stream);
+hipError_t launch_grad_norm(const double *sums, int n, const GradNormOut &o, hipStream_t stream);
+hipError_t launch_grad_norm_few(const GradBatch &b, const GradNormOut &o, hipStream_t stream);
+hipError_t launch_grad_finish(const GradNormOut &o, hipStream_t stream);
+hipError_t launch_grad_scale(const GradBatch &b, const mx_grad_norm_info *info, hipStream_t stream);
 hipError_t launch_dequantize(const uint8_t *q, const uint8_t *s, int64_t rows, int64_t length,
                              mx_layout layout, float *out, int64_t ldo, hipStream_t stream);
 hipError_t launch_measure_mfma(int fmt_a, int fmt_b, const void *ops, int workgroups, int64_t iters, float *out,
