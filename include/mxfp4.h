@@ -462,6 +462,37 @@ mx_status mx_gemm_a4w4_grouped_wgrad(int64_t M, int64_t N, int64_t K, const int3
                                      int64_t group_stride, hipStream_t stream);
 
 /*
+ * A whole layer of gated experts for a few tokens (decoding), two launches:
+ *   y_t = sum_j w_tj * D_e (silu(G_e x_t) * (U_e x_t)),   e = ids[t][j]
+ * with bf16 activations on the experts' MXFP4 weights, fp32 sums; silu(v) =
+ * v / (1 + exp(-v)), the product with U_e x_t rounded to bf16 before D_e.
+ *   x: tokens x K bf16, stride ldx.  ids: device int32, tokens x topk; an id
+ *     outside [0, experts) counts nothing (an expert that lives elsewhere), one
+ *     that a token names more than once counts with the sum of its weights.
+ *     weights: device fp32, tokens x topk.
+ *   W1: `experts` tiled blobs of 2 * inner rows along K one behind the other, G_e
+ *     in rows [0, inner), U_e behind it; W2: `experts` tiled blobs of K rows
+ *     along `inner`: the row-wise grouped blobs of mx_quantize_grouped.
+ *     Elements that bf16 holds as subnormal numbers may count as 0.
+ *   y: tokens x K of out_dtype, stride ldy; every row is written, 0 for a token
+ *     without experts.  The values of one token do not depend on the others'.
+ *   workspace: mx_experts_a16w4_bytes bytes, 16-byte aligned; calls that share
+ *     one must not overlap.
+ * Limits: tokens <= 64, topk <= 32, experts <= 1024, one expert's blob below 2
+ * GiB; for more tokens the grouped calls above.  tokens == 0 or K == 0 is a
+ * no-op; topk == 0 or inner == 0 writes zeros.
+ * Requires x, y, W1, W2, their scales and the workspace 16-byte aligned, ids and
+ * weights 4-byte aligned, ldx % 8 == 0 and ldy % 8 == 0.
+ * Errors: INVALID_ARGUMENT, MISALIGNED, UNSUPPORTED (layout, out_dtype, sizes),
+ * DEVICE_UNSUPPORTED, HIP.
+ */
+mx_status mx_experts_a16w4_bytes(int64_t tokens, int64_t inner, int topk, size_t *bytes);
+mx_status mx_experts_a16w4(int64_t tokens, int64_t K, int64_t inner, int experts, int topk, const void *x,
+                           int64_t ldx, const int32_t *ids, const float *weights, const void *W1,
+                           const void *W1_scale, const void *W2, const void *W2_scale, mx_layout layout,
+                           mx_dtype out_dtype, void *y, int64_t ldy, void *workspace, hipStream_t stream);
+
+/*
  * ---- AdamW over many tensors ----
  * One step of AdamW (Loshchilov and Hutter, decoupled weight decay) for every
  * tensor of a table.  Per element, in fp32 with each operation rounded by

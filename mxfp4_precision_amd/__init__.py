@@ -47,6 +47,7 @@ EXPORTED = ("mx_blob_bytes", "mx_quantize_rowwise", "mx_quantize_dual", "mx_gemm
             "mx_adamw", "mx_adamw_step_values",
             "mx_f8_b128_blob_bytes", "mx_quantize_fp8_b128", "mx_gemm_f8_b128", "mx_linear_f8_b128_bytes",
             "mx_linear_f8_b128", "mx_grad_norm_bytes", "mx_grad_norm", "mx_grad_norm_finish", "mx_clip_grads",
+            "mx_experts_a16w4_bytes", "mx_experts_a16w4",
             "mx_measure_mfma", "mx_set_device_arch_override", "mx_status_string", "mx_last_error")
 
 
@@ -167,6 +168,8 @@ def lib() -> ctypes.CDLL:
     L.mx_gemm_f8_b128.argtypes = [i32, i32, i64, i64, i64, i32, vp, vp, i32, vp, vp, i32, i32, vp, vp, i64, vp]
     L.mx_linear_f8_b128_bytes.argtypes = [i64, i64, szp]
     L.mx_linear_f8_b128.argtypes = [i64, i64, i64, i32, vp, i64, i32, vp, vp, i32, i32, vp, vp, i64, vp, vp]
+    L.mx_experts_a16w4_bytes.argtypes = [i64, i64, i32, szp]
+    L.mx_experts_a16w4.argtypes = [i64, i64, i64, i32, i32, vp, i64, vp, vp, vp, vp, vp, vp, i32, i32, vp, i64, vp, vp]
     gradp, f64 = ctypes.POINTER(mx_grad_tensor), ctypes.c_double
     L.mx_grad_norm_bytes.argtypes = [i64, szp]
     L.mx_grad_norm.argtypes = [gradp, i64, f64, f64, vp, vp, vp, vp]
@@ -233,6 +236,15 @@ def _room(workspace, need, *sizes):
         have = workspace.numel() * workspace.element_size()
         if not workspace.is_contiguous() or have < need(*sizes):
             raise ValueError("the workspace needs %d contiguous bytes, the tensor has %d" % (need(*sizes), have))
+
+
+def _f32ptr(p, count: int) -> Optional[int]:
+    """A device pointer to `count` float32 values, as _i32ptr."""
+    if p is not None and not isinstance(p, int) and hasattr(p, "data_ptr"):
+        if str(p.dtype) != "torch.float32" or not p.is_contiguous() or p.numel() < count:
+            raise TypeError("a contiguous float32 tensor of at least %d values is required, got %s of %s"
+                            % (count, p.dtype, tuple(p.shape)))
+    return _dptr(p)
 
 
 def _hptr(p) -> Optional[int]:
@@ -420,6 +432,23 @@ def mx_gemm_a4w4_grouped_wgrad(M: int, N: int, K: int, group_ends, groups: int, 
     _check(L.mx_gemm_a4w4_grouped_wgrad(M, N, K, _i32ptr(group_ends, groups), groups, _dptr(A), _dptr(A_scale),
                                         _dptr(B), _dptr(B_scale), layout, out_dtype, _dptr(C), ldc, group_stride,
                                         _stream(stream)))
+
+
+def mx_experts_a16w4_bytes(tokens: int, inner: int, topk: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().mx_experts_a16w4_bytes(tokens, inner, topk, ctypes.byref(n)))
+    return n.value
+
+
+def mx_experts_a16w4(tokens: int, K: int, inner: int, experts: int, topk: int, x, ldx: int, ids, weights, W1, W1_scale,
+                     W2, W2_scale, layout: int, out_dtype: int, y, ldy: int, workspace, stream=None):
+    """ids, weights: int32 and float32 of tokens * topk values.  workspace: a tensor or pointer of
+    mx_experts_a16w4_bytes(tokens, inner, topk) bytes; a shorter tensor is refused."""
+    _room(workspace, mx_experts_a16w4_bytes, tokens, inner, topk)
+    _check(lib().mx_experts_a16w4(tokens, K, inner, experts, topk, _dptr(x), ldx, _i32ptr(ids, tokens * topk),
+                                  _f32ptr(weights, tokens * topk), _dptr(W1), _dptr(W1_scale), _dptr(W2),
+                                  _dptr(W2_scale), layout, out_dtype, _dptr(y), ldy, _dptr(workspace),
+                                  _stream(stream)))
 
 
 def mx_adamw(tensors, count: int, opts: mx_adamw_opts, stream=None):

@@ -17,8 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmxfp4.so")
 SOURCES = ["api.cpp", "layout.cpp", "quantize.hip", "quantize_fp8.hip", "gemm.hip", "gemm_grouped.hip",
-           "quantize_f8_b128.hip", "gemm_f8_b128.hip", "adamw.hip",
-           "grad_norm.hip", "convert.hip", "dequantize.hip", "measure.hip"]
+           "quantize_f8_b128.hip", "gemm_f8_b128.hip", "experts_a16w4.hip",
+           "adamw.hip", "grad_norm.hip", "convert.hip", "dequantize.hip", "measure.hip"]
 ARCH = "gfx950"
 # The Python extension that converts the arguments of the hottest calls (host code).
 MARSHAL = os.path.join(HERE, "_marshal.so")

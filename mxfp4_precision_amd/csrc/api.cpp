@@ -749,6 +749,84 @@ mx_status mx_gemm_a4w4_grouped_wgrad(int64_t M, int64_t N, int64_t K, const int3
 
 namespace {
 
+mx_status check_experts(int64_t tokens, int64_t inner, int topk) {
+    if (tokens < 0 || inner < 0 || topk < 0)
+        return fail(MX_ERR_INVALID_ARGUMENT, "negative size tokens=%lld inner=%lld topk=%d", (long long)tokens,
+                    (long long)inner, topk);
+    if (tokens > mx::kExpertTokens || topk > mx::kExpertTopk)
+        return fail(MX_ERR_UNSUPPORTED, "tokens=%lld topk=%d: at most %d tokens and topk %d (more: the grouped calls)",
+                    (long long)tokens, topk, mx::kExpertTokens, mx::kExpertTopk);
+    if (inner >= (int64_t(1) << 24)) return fail(MX_ERR_UNSUPPORTED, "inner=%lld must stay below 2^24", (long long)inner);
+    return MX_SUCCESS;
+}
+
+// Parts of the workspace in bytes: counters, partial sums, activations.
+struct ExpertSpace {
+    size_t counters, sums, h;
+};
+ExpertSpace expert_space(int64_t tokens, int64_t inner, int topk) {
+    return {mx::kExpertSplits * sizeof(int), (size_t)tokens * mx::kExpertSplits * 16 * sizeof(float),
+            (size_t)(tokens * topk * mx::padded(inner)) * 2};
+}
+
+}  // namespace
+
+mx_status mx_experts_a16w4_bytes(int64_t tokens, int64_t inner, int topk, size_t *bytes) {
+    MX_TRY(check_experts(tokens, inner, topk));
+    if (!bytes) return fail(MX_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    const ExpertSpace s = expert_space(tokens, inner, topk);
+    *bytes = s.counters + s.sums + s.h;
+    return MX_SUCCESS;
+}
+
+mx_status mx_experts_a16w4(int64_t tokens, int64_t K, int64_t inner, int experts, int topk, const void *x, int64_t ldx,
+                           const int32_t *ids, const float *weights, const void *W1, const void *W1_scale,
+                           const void *W2, const void *W2_scale, mx_layout layout, mx_dtype out_dtype, void *y,
+                           int64_t ldy, void *workspace, hipStream_t stream) {
+    const char *name = "mx_experts_a16w4";
+    MX_TRY(check_experts(tokens, inner, topk));
+    if (K < 0) return fail(MX_ERR_INVALID_ARGUMENT, "negative K=%lld", (long long)K);
+    if (experts < 1) return fail(MX_ERR_INVALID_ARGUMENT, "experts=%d must be >= 1", experts);
+    if (experts > mx::kExpertsMost || K >= (int64_t(1) << 24))
+        return fail(MX_ERR_UNSUPPORTED, "experts=%d K=%lld: at most %d experts and K below 2^24", experts, (long long)K,
+                    mx::kExpertsMost);
+    MX_TRY(check_layout(layout));
+    if (layout != MX_LAYOUT_TILED) return fail(MX_ERR_UNSUPPORTED, "%s reads MX_LAYOUT_TILED blobs only", name);
+    if (out_dtype != MX_BF16 && out_dtype != MX_F32)
+        return fail(MX_ERR_UNSUPPORTED, "out_dtype %d (valid: MX_BF16=0, MX_F32=1)", (int)out_dtype);
+    MX_TRY(validate_x(x, tokens, K, ldx));
+    if (ldy < K || ldy < 1) return fail(MX_ERR_INVALID_ARGUMENT, "ldy=%lld must be >= max(K, 1)", (long long)ldy);
+    if (!y || !workspace) return fail(MX_ERR_INVALID_ARGUMENT, "y or workspace is NULL");
+    if (topk > 0 && (!ids || !weights)) return fail(MX_ERR_INVALID_ARGUMENT, "ids or weights is NULL");
+    if (inner > 0 && (!W1 || !W1_scale || !W2 || !W2_scale))
+        return fail(MX_ERR_INVALID_ARGUMENT, "a weight pointer is NULL");
+    if (!aligned16(y) || !aligned16(workspace) || !aligned16(W1) || !aligned16(W1_scale) || !aligned16(W2) ||
+        !aligned16(W2_scale))
+        return fail(MX_ERR_MISALIGNED, "y, the weights and the workspace must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(ids) & 3u) || (reinterpret_cast<uintptr_t>(weights) & 3u))
+        return fail(MX_ERR_MISALIGNED, "ids and weights must be 4-byte aligned");
+    if (ldy % 8) return fail(MX_ERR_MISALIGNED, "ldy=%lld must be a multiple of 8", (long long)ldy);
+    // (a grid of 256-thread workgroups must stay below 2^32 threads)
+    if ((int64_t)experts * (mx::padded(inner) / 16) >= (int64_t(1) << 24))
+        return fail(MX_ERR_UNSUPPORTED, "experts=%d inner=%lld: too many row tiles", experts, (long long)inner);
+    MX_TRY(check_blob_limit(name, "W1 (one expert)", 2 * inner, mx::padded(K) / 2));
+    MX_TRY(check_blob_limit(name, "W2 (one expert)", K, mx::padded(inner) / 2));
+    if (tokens == 0 || K == 0) return MX_SUCCESS;
+    MX_TRY(check_device());
+    const ExpertSpace s = expert_space(tokens, inner, topk);
+    uint8_t *w = static_cast<uint8_t *>(workspace);
+    // (without activations there is nothing to sum: zeros)
+    const mx::ExpertsArgs a{(int)tokens, experts, inner > 0 ? topk : 0, K, inner, ldx, ldy,
+                            static_cast<const uint16_t *>(x), ids, weights, static_cast<const uint8_t *>(W1),
+                            static_cast<const uint8_t *>(W1_scale), static_cast<const uint8_t *>(W2),
+                            static_cast<const uint8_t *>(W2_scale), y, reinterpret_cast<int *>(w),
+                            reinterpret_cast<float *>(w + s.counters),
+                            reinterpret_cast<uint16_t *>(w + s.counters + s.sums)};
+    return check_launch(mx::launch_experts(a, out_dtype, stream), name);
+}
+
+namespace {
+
 mx_adamw_step step_of(const mx_adamw_opts &o) {
     mx_adamw_step s;
     s.grad_scale = (float)o.grad_scale;

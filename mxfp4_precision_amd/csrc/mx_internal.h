@@ -79,6 +79,29 @@ struct F8LinearArgs {
     F8GemmArgs g;               // A, As: the workspace's blob, if the form needs one
 };
 
+// A layer of experts for a few tokens.
+constexpr int kExpertTokens = 64, kExpertTopk = 32, kExpertsMost = 1024;
+constexpr int kExpertSplits = 1024;   // most workgroups of the down product where it is split
+struct ExpertsArgs {
+    int tokens, experts, topk;
+    int64_t K, inner, ldx, ldy;
+    const uint16_t *x;
+    const int32_t *ids;
+    const float *weights;
+    const uint8_t *W1, *W1s, *W2, *W2s;
+    void *y;
+    int *counters;              // kExpertSplits, zeroed by the first kernel
+    float *sums;                // kExpertSplits x 16 x tokens
+    uint16_t *h;                // tokens * topk rows of padded(inner) activations
+};
+// Workgroups that share a row tile of the down product.
+inline int expert_splits(int slots, int64_t K, int64_t inner) {
+    const int64_t tiles = cdiv(K, 16), atoms = slots * (padded(inner) / 128);
+    int64_t n = atoms / 32;     // 8 waves, four atoms each
+    if (n > kExpertSplits / tiles) n = kExpertSplits / tiles;
+    return n > 1 ? (int)n : 1;
+}
+
 // Descriptors of one AdamW launch, passed as kernel arguments.
 struct AdamwItem {
     void *param;
@@ -166,6 +189,7 @@ hipError_t launch_gemm_grouped(const GroupedGemmArgs &a, hipStream_t stream);
 hipError_t launch_gemm_grouped_wgrad(const GroupedGemmArgs &a, hipStream_t stream);
 int64_t adamw_chunks(int64_t numel);   // workgroups that numel elements take
 hipError_t launch_adamw(const AdamwBatch &b, bool p32, bool g32, bool s8, bool sr, hipStream_t stream);
+hipError_t launch_experts(const ExpertsArgs &a, mx_dtype out_dtype, hipStream_t stream);
 hipError_t launch_grad_sums(const GradBatch &b, double *sums, hipStream_t stream);
 hipError_t launch_grad_norm(const double *sums, int n, const GradNormOut &o, hipStream_t stream);
 hipError_t launch_grad_norm_few(const GradBatch &b, const GradNormOut &o, hipStream_t stream);
