@@ -478,7 +478,7 @@ mx_status mx_gemm_a4w4_grouped_wgrad(int64_t M, int64_t N, int64_t K, const int3
  *     without experts.  The values of one token do not depend on the others'.
  *   workspace: mx_experts_a16w4_bytes bytes, 16-byte aligned; calls that share
  *     one must not overlap.
- * Limits: tokens <= 64, topk <= 32, experts <= 1024, one expert's blob below 2
+ * Limits: tokens <= 64, topk <= 32, experts <= 1024, x and one expert's blob below 2
  * GiB; for more tokens the grouped calls above.  tokens == 0 or K == 0 is a
  * no-op; topk == 0 or inner == 0 writes zeros.
  * Requires x, y, W1, W2, their scales and the workspace 16-byte aligned, ids and

@@ -766,7 +766,7 @@ struct ExpertSpace {
 };
 ExpertSpace expert_space(int64_t tokens, int64_t inner, int topk) {
     return {mx::kExpertSplits * sizeof(int), (size_t)tokens * mx::kExpertSplits * 16 * sizeof(float),
-            (size_t)(tokens * topk * mx::padded(inner)) * 2};
+            (size_t)(mx::expert_tiles(tokens * topk) * 16 * mx::padded(inner)) * 2};
 }
 
 }  // namespace
@@ -806,6 +806,8 @@ mx_status mx_experts_a16w4(int64_t tokens, int64_t K, int64_t inner, int experts
     if ((reinterpret_cast<uintptr_t>(ids) & 3u) || (reinterpret_cast<uintptr_t>(weights) & 3u))
         return fail(MX_ERR_MISALIGNED, "ids and weights must be 4-byte aligned");
     if (ldy % 8) return fail(MX_ERR_MISALIGNED, "ldy=%lld must be a multiple of 8", (long long)ldy);
+    if (ldx >= (int64_t(1) << 24) || ((tokens - 1) * ldx + K) * 2 >= (int64_t(1) << 31) - 4)
+        return fail(MX_ERR_UNSUPPORTED, "%s: x spans 2 GiB or more", name);
     // (a grid of 256-thread workgroups must stay below 2^32 threads)
     if ((int64_t)experts * (mx::padded(inner) / 16) >= (int64_t(1) << 24))
         return fail(MX_ERR_UNSUPPORTED, "experts=%d inner=%lld: too many row tiles", experts, (long long)inner);

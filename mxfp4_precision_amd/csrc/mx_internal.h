@@ -81,7 +81,7 @@ struct F8LinearArgs {
 
 // A layer of experts for a few tokens.
 constexpr int kExpertTokens = 64, kExpertTopk = 32, kExpertsMost = 1024;
-constexpr int kExpertSplits = 1024;   // most workgroups of the down product where it is split
+constexpr int kExpertSplits = 384;   // most workgroups of the down product where it is split
 struct ExpertsArgs {
     int tokens, experts, topk;
     int64_t K, inner, ldx, ldy;
@@ -92,12 +92,23 @@ struct ExpertsArgs {
     void *y;
     int *counters;              // kExpertSplits, zeroed by the first kernel
     float *sums;                // kExpertSplits x 16 x tokens
-    uint16_t *h;                // tokens * topk rows of padded(inner) activations
+    uint16_t *h;                // expert_tiles x 16 x padded(inner) activations
 };
-// Workgroups that share a row tile of the down product.
-inline int expert_splits(int slots, int64_t K, int64_t inner) {
-    const int64_t tiles = cdiv(K, 16), atoms = slots * (padded(inner) / 128);
-    int64_t n = atoms / 32;     // 8 waves, four atoms each
+// Column tiles of 16 tokens that pairs can make: one for each expert that they
+// name, and one more for every 16.
+inline int64_t expert_tiles(int64_t pairs) { return (pairs < kExpertsMost ? pairs : kExpertsMost) + pairs / 16; }
+// Tiles of 16 rows of the up product that a workgroup takes: two where an expert
+// can have 4 tokens on average, which halves the reading of activations.  In us,
+// one / two: 64 tokens, 8 of 64 experts, 2048 x 1024 38 / 32; 16 tokens, 4 of 32,
+// 4096 x 1536 28.6 / 27.5; 5 tokens 5.9 / 7.1, 1 token 7.5 / 9.2.
+inline int expert_row_tiles(int pairs, int slots) { return pairs >= 4 * slots ? 2 : 1; }
+// Workgroups that share a row tile of the down product: 1.5 workgroups per CU
+// (64 tokens, 8 of 64 experts, 2048 x 1024, 128 row tiles: 2, 3, 4 and 8 of them
+// 33, 29, 31 and 37 us; 16 tokens, 256 row tiles: 1, 3 and 4 18, 22 and 24 us),
+// each with four atoms for each of its 8 waves at least.
+inline int expert_splits(int slots, int64_t tiles, int64_t inner) {
+    const int64_t atoms = slots * (padded(inner) / 128);
+    int64_t n = atoms / 32;
     if (n > kExpertSplits / tiles) n = kExpertSplits / tiles;
     return n > 1 ? (int)n : 1;
 }
