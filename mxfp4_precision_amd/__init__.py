@@ -124,7 +124,9 @@ def grad_table(rows):
 
 
 try:
-    from . import _marshal      # converts the arguments of the grouped calls (csrc/marshal.cpp)
+    from . import _marshal      # converts the arguments of the calls that run most often (csrc/marshal.cpp)
+    if not hasattr(_marshal, "clip_grads"):
+        _marshal = None         # an older build's, loaded before build() replaced it
 except ImportError:
     _marshal = None             # the same conversions in Python
 
@@ -189,8 +191,11 @@ def lib() -> ctypes.CDLL:
             getattr(L, name).restype = i32     # mx_status
     if _marshal is not None:
         address = lambda f: ctypes.cast(f, vp).value  # noqa: E731
-        _marshal.bind(address(L.mx_quantize_grouped), address(L.mx_gemm_a4w4_grouped),
-                      address(L.mx_gemm_a4w4_grouped_wgrad), _dptr, _i32ptr, _stream, mx_quant_opts)
+        names = ("mx_quantize_grouped", "mx_gemm_a4w4_grouped", "mx_gemm_a4w4_grouped_wgrad", "mx_quantize_fp8_b128",
+                 "mx_gemm_f8_b128", "mx_linear_f8_b128", "mx_linear_f8_b128_bytes", "mx_experts_a16w4",
+                 "mx_experts_a16w4_bytes", "mx_grad_norm", "mx_grad_norm_bytes", "mx_clip_grads")
+        _marshal.bind(tuple(address(getattr(L, n)) for n in names), _dptr, _i32ptr, _f32ptr, _stream, _room,
+                      mx_quant_opts, mx_grad_tensor)
     _lib = L
     return L
 
@@ -230,12 +235,19 @@ def _i32ptr(p, count: int) -> Optional[int]:
     return _dptr(p)
 
 
-def _room(workspace, need, *sizes):
-    """A tensor given as workspace has need(*sizes) bytes at least (an int's caller vouches for it)."""
+def _room(workspace, need: int):
+    """A tensor given as workspace has `need` bytes at least (an int's caller vouches for it)."""
     if workspace is not None and not isinstance(workspace, int) and hasattr(workspace, "data_ptr"):
         have = workspace.numel() * workspace.element_size()
-        if not workspace.is_contiguous() or have < need(*sizes):
-            raise ValueError("the workspace needs %d contiguous bytes, the tensor has %d" % (need(*sizes), have))
+        if not workspace.is_contiguous() or have < need:
+            raise ValueError("the workspace needs %d contiguous bytes, the tensor has %d" % (need, have))
+
+
+def _space(workspace, function, *sizes):
+    """_room for the bytes that `function` gives; sizes that it refuses are the call's to report."""
+    n = ctypes.c_size_t()
+    if function(*sizes, ctypes.byref(n)) == MX_SUCCESS:
+        _room(workspace, n.value)
 
 
 def _f32ptr(p, count: int) -> Optional[int]:
@@ -368,14 +380,24 @@ def mx_f8_b128_blob_bytes(rows: int, length: int, layout: int) -> Tuple[int, int
 
 def mx_quantize_fp8_b128(x, M: int, N: int, ldx: int, row_fmt: int, row_opts, col_fmt: int, col_opts, layout: int,
                          q_row, s_row, q_col=None, s_col=None, stream=None):
-    _check(lib().mx_quantize_fp8_b128(_dptr(x), M, N, ldx, row_fmt, _opts(row_opts), col_fmt, _opts(col_opts), layout,
-                                      _dptr(q_row), _dptr(s_row), _dptr(q_col), _dptr(s_col), _stream(stream)))
+    L = lib()
+    if _marshal is not None:
+        _check(_marshal.quantize_fp8_b128(x, M, N, ldx, row_fmt, row_opts, col_fmt, col_opts, layout, q_row, s_row,
+                                          q_col, s_col, stream))
+        return
+    _check(L.mx_quantize_fp8_b128(_dptr(x), M, N, ldx, row_fmt, _opts(row_opts), col_fmt, _opts(col_opts), layout,
+                                  _dptr(q_row), _dptr(s_row), _dptr(q_col), _dptr(s_col), _stream(stream)))
 
 
 def mx_gemm_f8_b128(transA: int, transB: int, M: int, N: int, K: int, fmt_a: int, A, A_scale, fmt_b: int, B, B_scale,
                     layout: int, out_dtype: int, bias, C, ldc: int, stream=None):
-    _check(lib().mx_gemm_f8_b128(transA, transB, M, N, K, fmt_a, _dptr(A), _dptr(A_scale), fmt_b, _dptr(B),
-                                 _dptr(B_scale), layout, out_dtype, _dptr(bias), _dptr(C), ldc, _stream(stream)))
+    L = lib()
+    if _marshal is not None:
+        _check(_marshal.gemm_f8_b128(transA, transB, M, N, K, fmt_a, A, A_scale, fmt_b, B, B_scale, layout, out_dtype,
+                                     bias, C, ldc, stream))
+        return
+    _check(L.mx_gemm_f8_b128(transA, transB, M, N, K, fmt_a, _dptr(A), _dptr(A_scale), fmt_b, _dptr(B),
+                             _dptr(B_scale), layout, out_dtype, _dptr(bias), _dptr(C), ldc, _stream(stream)))
 
 
 def mx_linear_f8_b128_bytes(M: int, K: int) -> int:
@@ -387,9 +409,14 @@ def mx_linear_f8_b128_bytes(M: int, K: int) -> int:
 def mx_linear_f8_b128(M: int, N: int, K: int, fmt_x: int, x, ldx: int, fmt_w: int, W, W_scale, layout: int,
                       out_dtype: int, bias, y, ldy: int, workspace, stream=None):
     """workspace: a tensor or pointer of mx_linear_f8_b128_bytes(M, K) bytes; a shorter tensor is refused."""
-    _room(workspace, mx_linear_f8_b128_bytes, M, K)
-    _check(lib().mx_linear_f8_b128(M, N, K, fmt_x, _dptr(x), ldx, fmt_w, _dptr(W), _dptr(W_scale), layout, out_dtype,
-                                   _dptr(bias), _dptr(y), ldy, _dptr(workspace), _stream(stream)))
+    L = lib()
+    if _marshal is not None:
+        _check(_marshal.linear_f8_b128(M, N, K, fmt_x, x, ldx, fmt_w, W, W_scale, layout, out_dtype, bias, y, ldy,
+                                       workspace, stream))
+        return
+    _space(workspace, L.mx_linear_f8_b128_bytes, M, K)
+    _check(L.mx_linear_f8_b128(M, N, K, fmt_x, _dptr(x), ldx, fmt_w, _dptr(W), _dptr(W_scale), layout, out_dtype,
+                               _dptr(bias), _dptr(y), ldy, _dptr(workspace), _stream(stream)))
 
 
 def mx_grouped_blob_bytes(M: int, N: int, groups: int) -> Tuple[int, int, int, int]:
@@ -444,11 +471,15 @@ def mx_experts_a16w4(tokens: int, K: int, inner: int, experts: int, topk: int, x
                      W2, W2_scale, layout: int, out_dtype: int, y, ldy: int, workspace, stream=None):
     """ids, weights: int32 and float32 of tokens * topk values.  workspace: a tensor or pointer of
     mx_experts_a16w4_bytes(tokens, inner, topk) bytes; a shorter tensor is refused."""
-    _room(workspace, mx_experts_a16w4_bytes, tokens, inner, topk)
-    _check(lib().mx_experts_a16w4(tokens, K, inner, experts, topk, _dptr(x), ldx, _i32ptr(ids, tokens * topk),
-                                  _f32ptr(weights, tokens * topk), _dptr(W1), _dptr(W1_scale), _dptr(W2),
-                                  _dptr(W2_scale), layout, out_dtype, _dptr(y), ldy, _dptr(workspace),
-                                  _stream(stream)))
+    L = lib()
+    if _marshal is not None:
+        _check(_marshal.experts_a16w4(tokens, K, inner, experts, topk, x, ldx, ids, weights, W1, W1_scale, W2, W2_scale,
+                                      layout, out_dtype, y, ldy, workspace, stream))
+        return
+    _space(workspace, L.mx_experts_a16w4_bytes, tokens, inner, topk)
+    _check(L.mx_experts_a16w4(tokens, K, inner, experts, topk, _dptr(x), ldx, _i32ptr(ids, tokens * topk),
+                              _f32ptr(weights, tokens * topk), _dptr(W1), _dptr(W1_scale), _dptr(W2), _dptr(W2_scale),
+                              layout, out_dtype, _dptr(y), ldy, _dptr(workspace), _stream(stream)))
 
 
 def mx_adamw(tensors, count: int, opts: mx_adamw_opts, stream=None):
@@ -480,9 +511,13 @@ def mx_grad_norm(tensors, count: int, max_norm: float, grad_scale: float, worksp
     """tensors: an array of grad_table.  info: a GPU tensor that holds an mx_grad_norm_info (16 bytes: the sum of
     squares as a float64, norm and scale as float32); step: one that holds an mx_adamw_step, or None.  workspace: a
     tensor or pointer of mx_grad_norm_bytes(count) bytes; a shorter tensor is refused."""
-    _room(workspace, mx_grad_norm_bytes, count)
-    _check(lib().mx_grad_norm(_table(tensors, count), count, max_norm, grad_scale, _dptr(workspace), _dptr(info),
-                              _dptr(step), _stream(stream)))
+    L = lib()
+    if _marshal is not None:
+        _check(_marshal.grad_norm(tensors, count, max_norm, grad_scale, workspace, info, step, stream))
+        return
+    _space(workspace, L.mx_grad_norm_bytes, count)
+    _check(L.mx_grad_norm(_table(tensors, count), count, max_norm, grad_scale, _dptr(workspace), _dptr(info),
+                          _dptr(step), _stream(stream)))
 
 
 def mx_grad_norm_finish(max_norm: float, grad_scale: float, info, step=None, stream=None):
@@ -490,7 +525,11 @@ def mx_grad_norm_finish(max_norm: float, grad_scale: float, info, step=None, str
 
 
 def mx_clip_grads(tensors, count: int, info, stream=None):
-    _check(lib().mx_clip_grads(_table(tensors, count), count, _dptr(info), _stream(stream)))
+    L = lib()
+    if _marshal is not None:
+        _check(_marshal.clip_grads(tensors, count, info, stream))
+        return
+    _check(L.mx_clip_grads(_table(tensors, count), count, _dptr(info), _stream(stream)))
 
 
 def mx_layout_convert(to_tiled: int, rows: int, length: int, q_src, s_src, q_dst, s_dst, stream=None):

@@ -10,9 +10,13 @@ OK = mx.MX_ERR_DEVICE_UNSUPPORTED    # passed every check
 INVALID, MISALIGNED, UNSUPPORTED = mx.MX_ERR_INVALID_ARGUMENT, mx.MX_ERR_MISALIGNED, mx.MX_ERR_UNSUPPORTED
 
 
-@pytest.fixture(autouse=True)
-def _no_launch():
-    """The addresses here are never real: every valid call stops at the device check."""
+@pytest.fixture(autouse=True, params=["extension", "ctypes"])
+def _no_launch(request, monkeypatch):
+    """The addresses here are never real: every valid call stops at the device check.  Both conversions of the calls'
+    arguments."""
+    mx.lib()
+    if request.param == "ctypes":
+        monkeypatch.setattr(mx, "_marshal", None)
     mx.mx_set_device_arch_override("gfx000")
     yield
     mx.mx_set_device_arch_override(None)
