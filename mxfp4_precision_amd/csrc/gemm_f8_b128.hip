@@ -380,7 +380,7 @@ __device__ __forceinline__ void f8_store_private(const v16f (&acc)[C::kMB][C::kM
             const int r = 4 * s + (lane >> 4);
             const v4u_t v = *reinterpret_cast<const v4u_t *>(slot + r * 256 + (((lane & 15) ^ (r & 15)) * 16));
             const int row = row0 + 32 * p + 4 * s;
-            const uint32_t off = row < M && col < N ? (uint32_t)(row * ldc + col) * 2u : kOutOfRange;
+            const uint32_t off = row < M && col < N ? ((uint32_t)row * (uint32_t)ldc + (uint32_t)col) * 2u : kOutOfRange;
             __builtin_amdgcn_raw_buffer_store_b128(v, rC, off, 0, kCachePolicyNT);
         }
     }
@@ -739,12 +739,14 @@ hipError_t launch_formats(const F8GemmArgs &a, hipStream_t stream) {
             break;
         }
         case F8Form::kPersistent: {
-            const int tiles_m = (int)cdiv(a.M, 256), tiles_n = (int)cdiv(a.N, 256);
+            const int tiles_m = (int)cdiv(a.M, 256), tiles_n = (int)cdiv(a.N, 256), tiles = tiles_m * tiles_n;
+            const int cus = device_cu_count();
             if constexpr (OUT_BF16)
                 hipLaunchKernelGGL(a.bias ? (gemm_f8_b128_stream_kernel<F8Main, FA, FB, true>)
                                           : (gemm_f8_b128_stream_kernel<F8Main, FA, FB, false>),
-                                   dim3((unsigned)device_cu_count()), dim3(F8Main::kThreads), 0, stream, (int)a.M,
-                                   (int)a.N, (int)K_pad, tiles_m, tiles_n, kBandRows, a.A, a.As, a.B, a.Bs, a.bias, a.C, (int)a.ldc);
+                                   dim3((unsigned)(tiles < cus ? tiles : cus)), dim3(F8Main::kThreads), 0, stream,
+                                   (int)a.M, (int)a.N, (int)K_pad, tiles_m, tiles_n, kBandRows, a.A, a.As, a.B, a.Bs,
+                                   a.bias, a.C, (int)a.ldc);
             break;
         }
         case F8Form::kTiles256: {

@@ -1,10 +1,14 @@
 """FP8 with block scales of 128 on the CPU: blob sizes, refusals before any launch, and the form a size takes."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 
+import f8_cases
 import mxfp4_precision_amd as mx
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 A16 = 1 << 20
 T, C = mx.MX_LAYOUT_TILED, mx.MX_LAYOUT_CANONICAL
 OK = mx.MX_ERR_DEVICE_UNSUPPORTED    # passed every check
@@ -125,3 +129,46 @@ def test_tensors_on_the_host_and_short_workspaces_are_refused():
         gemm(bias=t)
     with pytest.raises(ValueError):
         linear(M=2000, ws=t)
+
+
+PROGRAM = r"""
+#include <cstdio>
+#include "gemm_f8_b128_forms.h"
+int main() {
+    long long M, N, K, ldc, bf16, cus;
+    const char *names[] = {"few", "128", "persistent", "256"};
+    while (scanf("%lld%lld%lld%lld%lld%lld", &M, &N, &K, &ldc, &bf16, &cus) == 6) {
+        mx::F8GemmArgs a{};
+        a.M = M; a.N = N; a.K = K; a.ldc = ldc; a.out_dtype = bf16 ? MX_BF16 : MX_F32;
+        puts(names[(int)mx::f8_gemm_form(a, (int)cus)]);
+    }
+}
+"""
+
+
+def test_forms(tmp_path):
+    """The form of each tested size, and both sides of the rules' borders."""
+    (tmp_path / "forms.cpp").write_text(PROGRAM)
+    exe = str(tmp_path / "forms")
+    subprocess.check_call(["g++", "-std=c++17", "-O1", "-D__HIP_PLATFORM_AMD__", "-isystem", "/opt/rocm/include",
+                           "-I", os.path.join(ROOT, "mxfp4_precision_amd", "csrc"), str(tmp_path / "forms.cpp"), "-o", exe])
+    ask = [(M, N, K, -(-N // 8) * 8, bf, 256) for M, N, K in f8_cases.SHAPES for bf in (1, 0)]
+    want = []
+    for form, shapes in f8_cases.FORMS.items():
+        want += [form, "256" if form == "persistent" else form] * len(shapes)
+    borders = [((64, 1 << 20, 128, 1 << 20, 1, 256), "few"), ((65, 1 << 20, 128, 1 << 20, 1, 256), "128"),
+               ((768, 2048, 512, 2048, 1, 256), "few"), ((768, 2049, 512, 2056, 1, 256), "128"),
+               # 775 tiles of 128 x 128 or one round of 256 x 256; 776
+               ((3200, 3968, 512, 3968, 1, 256), "128"), ((1024, 12416, 512, 12416, 1, 256), "persistent"),
+               # a second round for few tiles
+               ((4352, 4096, 512, 4096, 1, 256), "128"), ((4096, 4096, 512, 4096, 1, 256), "persistent"),
+               # 32-bit offsets into C
+               ((16384, 65528, 512, 65528, 1, 256), "persistent"), ((16384, 65536, 512, 65536, 1, 256), "256"),
+               # the number of CUs is unknown
+               ((1000, 1000, 512, 1000, 1, 0), "256"), ((16384, 16384, 512, 16384, 1, 0), "256"),
+               ((16, 1000, 512, 1000, 1, 0), "few")]
+    ask += [b[0] for b in borders]
+    want += [b[1] for b in borders]
+    out = subprocess.run([exe], input="\n".join(" ".join(map(str, a)) for a in ask), capture_output=True, text=True,
+                         check=True).stdout.split()
+    assert [(a, o) for a, o, w in zip(ask, out, want) if o != w] == []

@@ -8,6 +8,7 @@ torch = pytest.importorskip("torch")
 import mxfp4_precision_amd as mx
 from mxfp4_precision_amd import synth
 
+import f8_cases
 import f8_ref as ref
 from gpu_util import host, log, to_dev_bf16
 
@@ -172,24 +173,17 @@ def check_product(M, N, K, fa, fb, make, with_bias=False, what=""):
     assert torch.equal(out16[:M, :N], out[:M, :N].bfloat16()), what + ": bf16 is not the rounded fp32 output"
 
 
-PRODUCTS = [
-    # few rows
-    (1, 16, 128), (1, 1, 1), (3, 40, 200), (16, 256, 512), (17, 33, 640), (33, 70, 1100), (64, 96, 513), (50, 1000, 384),
-    (200, 100, 300), (1, 700, 5000),
-    # 128 x 128 tiles
-    (1500, 1500, 200), (1153, 1985, 1300), (2000, 1111, 520),
-    # 256 x 256 tiles, persistent where N is a multiple of 8 and the tiles outnumber the CUs
-    (2300, 2500, 600), (2304, 2560, 1024), (4000, 4300, 1100), (4360, 4104, 300), (8200, 4616, 513), (6000, 3601, 700),
-]
+PRODUCTS = f8_cases.SHAPES
 
 
 @pytest.mark.parametrize("shape", PRODUCTS, ids=str)
 def test_product(shape):
     M, N, K = shape
     small = M * N * K < 10 ** 7
-    for fa, fb in ((0, 0), (1, 0), (0, 1), (1, 1)) if small else ((0, 0), (1, 0)):
-        check_product(M, N, K, fa, fb, normal_codes, what="normal %d %d" % (fa, fb))
-    check_product(M, N, K, 0, 0, normal_codes, True, "bias")
+    for fa, fb in ((0, 0), (1, 0), (0, 1), (1, 1)):
+        check_product(M, N, K, fa, fb, normal_codes, (fa, fb) == (0, 1), "normal %d %d" % (fa, fb))
+    if small:
+        check_product(M, N, K, 0, 0, normal_codes, True, "bias")
     if small:
         for fa, fb in ((0, 0), (1, 0), (0, 1), (1, 1)):
             check_product(M, N, K, fa, fb, codes_of, what="codes %d %d" % (fa, fb))
@@ -248,3 +242,145 @@ def test_linear_with_non_finite_rows():
         keep = np.delete(np.arange(M), (1, 2))
         want = ref.product([v[keep] for v in ref.quantize(bits, 0, 0)], w, 0, 0)
         check_entries(got[keep], *want)
+
+
+# ------------------------------------------------------------------ borders
+@pytest.mark.parametrize("dtype", [mx.MX_BF16, mx.MX_F32])
+def test_sizes_of_zero(dtype):
+    bias = torch.arange(40, device="cuda", dtype=torch.bfloat16)
+    for add in (None, bias):
+        got, _ = run((None, None), (None, None), 70, 40, 0, 0, 0, dtype, add)
+        assert (got == (0 if add is None else bias.double().cpu().numpy())).all()
+        y = torch.full((70, 40), -1.0, dtype=torch.float32 if dtype == mx.MX_F32 else torch.bfloat16, device="cuda")
+        mx.mx_linear_f8_b128(70, 40, 0, 0, None, 8, 0, None, None, T, dtype, add, y, 40, None)
+        assert torch.equal(y.float(), torch.zeros(70, 40, device="cuda") if add is None else bias.float().expand(70, 40))
+
+
+def test_nan_scales_and_overflow():
+    """A scale of 0xFF gives NaN in its row or column and nowhere else; sums past bf16's range give Inf, in every
+    form."""
+    for M, N, K in ((5, 48, 256), (1500, 1500, 256), (4000, 4000, 256)):
+        a, b = normal_codes(M, K, 0, 1), normal_codes(N, K, 0, 2)
+        a[1][M // 2, 1] = 255
+        b[1][N - 1, 0] = 255
+        a[0][0, :], a[1][0, :] = 0x7E, 254 - 8         # 448 2^119
+        b[0][0, :], b[1][0, :] = 0x7E, 127
+        b[0][1, :], b[1][1, :] = 0xFE, 127
+        for dt in (mx.MX_F32, mx.MX_BF16):
+            got, _ = run(dev_blob(*a), dev_blob(*b), M, N, K, 0, 0, dt)
+            nan = np.zeros((M, N), bool)
+            nan[M // 2], nan[:, N - 1] = True, True
+            # (row 0: 448 2^119 times values of both signs sums to Inf - Inf in fp32 but where all have one sign)
+            assert (np.isnan(got[1:]) == nan[1:]).all()
+            assert got[0, 0] == np.inf and got[0, 1] == -np.inf
+            assert np.isfinite(got[1:][~nan[1:]]).all()
+
+
+def test_a_training_step_together_in_a_graph():
+    """Quantizers, the three products, the gradient's norm and AdamW, captured once and replayed on other inputs, equal
+    the same calls made one by one."""
+    tokens, k, n = 300, 520, 392
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    normal = lambda *s: torch.randn(*s, device="cuda", generator=gen)  # noqa: E731
+    x, dy = normal(tokens, k).bfloat16(), (normal(tokens, n) * 1e-2).bfloat16()
+    master = normal(n, k) * 0.02
+    w = master.bfloat16()
+    both = lambda r, l: (*mx.empty_f8_b128_blob(r, l, T), *mx.empty_f8_b128_blob(l, r, T))  # noqa: E731
+    bx, bw, bd = both(tokens, k), both(n, k), both(tokens, n)
+    y, dx = torch.empty(tokens, n, device="cuda", dtype=torch.bfloat16), torch.empty(tokens, k, device="cuda", dtype=torch.bfloat16)
+    dw, m, v = (torch.zeros(n, k, device="cuda") for _ in range(3))
+    table = mx.grad_table([mx.grad_tensor(dw, dw.numel(), mx.MX_F32)])
+    space = torch.empty(mx.mx_grad_norm_bytes(1), dtype=torch.uint8, device="cuda")
+    info = torch.zeros(2, dtype=torch.float64, device="cuda")
+    h = dict(lr=1e-2, step=1, grad_dtype=mx.MX_F32)
+    step = torch.frombuffer(bytearray(mx.mx_adamw_step_values(mx.adamw_opts(**h))), dtype=torch.uint8).cuda()
+    adamw = mx.adamw_table([mx.adamw_tensor(master, dw, m, v, master.numel(), param_copy=w)])
+    square = mx.quant_opts(use_2d_block=True)
+    eval_y = torch.empty(7, n, device="cuda", dtype=torch.bfloat16)
+    eval_space = torch.empty(max(mx.mx_linear_f8_b128_bytes(7, k), 1), dtype=torch.uint8, device="cuda")
+
+    def train():
+        mx.mx_quantize_fp8_b128(x, tokens, k, k, 0, None, 0, None, T, *bx)
+        mx.mx_quantize_fp8_b128(w, n, k, k, 0, square, 0, square, T, *bw)
+        mx.mx_gemm_f8_b128(0, 1, tokens, n, k, 0, bx[0], bx[1], 0, bw[0], bw[1], T, mx.MX_BF16, None, y, n)
+        mx.mx_quantize_fp8_b128(dy, tokens, n, n, 1, None, 1, None, T, *bd)
+        mx.mx_gemm_f8_b128(0, 1, tokens, k, n, 1, bd[0], bd[1], 0, bw[2], bw[3], T, mx.MX_BF16, None, dx, k)
+        mx.mx_gemm_f8_b128(0, 1, n, k, tokens, 1, bd[2], bd[3], 0, bx[2], bx[3], T, mx.MX_F32, None, dw, k)
+        mx.mx_grad_norm(table, 1, 1e-3, 1.0, space, info, step)
+        mx.mx_adamw(adamw, 1, mx.adamw_opts(**h, device_step=step))
+        mx.mx_linear_f8_b128(7, n, k, 0, x, k, 0, bw[0], bw[1], T, mx.MX_BF16, None, eval_y, n, eval_space)
+
+    state = (x, dy, master, w, m, v)
+    outputs = (y, dx, dw, master, w, m, v, eval_y)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        train()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        train()
+    torch.cuda.synchronize()
+    for turn in range(4):
+        fresh = [normal(*t.shape).mul_(0.02).abs_().to(t.dtype) if t is v else normal(*t.shape).mul_(0.02).to(t.dtype)
+                 for t in state]
+        for t, f in zip(state, fresh):
+            t.copy_(f)
+        train()
+        want = [t.clone() for t in outputs]
+        norm = info.view(torch.float32)[2].item()
+        assert abs(norm - dw.double().norm().item()) <= 2.0 ** -23 * norm and norm > 1e-3
+        for t, f in zip(state, fresh):
+            t.copy_(f)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outputs, want):
+            assert torch.equal(a, b), turn
+
+
+def test_gradients_against_differences():
+    """dx and dw are the products' own gradients: differences of sum(y * dy) over steps of x and w that the codes hold
+    exactly."""
+    rng = np.random.default_rng(3)
+    tokens, k, n = 48, 160, 72
+    # values k/8 with |k| <= 8 and a 1 in every block: codes hold them and their changes by 1/8 to 1
+    grid = lambda *s: np.round(rng.uniform(-7, 7, s)) / 8  # noqa: E731
+    x, w, dy = grid(tokens, k), grid(n, k), grid(tokens, n)
+    for t in (x, w, dy):
+        t[0, :], t[:, 0] = 1.0, 1.0
+        t[:, 128 if t.shape[1] > 128 else 1] = 1.0
+
+    def product(a, b, rows, cols, inner):
+        blobs = []
+        for t in (a, b):
+            bits = synth.bf16_bits(t.astype(np.float32)).reshape(t.shape)
+            r, _ = quantize(bits, 0, 0, col=False)
+            blobs.append([r[0], r[1]])
+        return run(blobs[0], blobs[1], rows, cols, inner, 0, 0, mx.MX_F32)[0]
+
+    loss = lambda x_, w_: (product(x_, w_, tokens, n, k) * dy).sum()  # noqa: E731
+    dx = product(dy, np.ascontiguousarray(w.T), tokens, k, n)
+    dw = product(np.ascontiguousarray(dy.T), np.ascontiguousarray(x.T), n, k, tokens)
+    # sums of products of multiples of 1/64 below 2^10: exact in fp32, and so are the matrix instruction's (products of
+    # up to 7 bits lie within 13 bits of the largest)
+    assert (dx == dy @ w).all() and (dw == dy.T @ x).all()
+    for i, j in ((3, 5), (47, 159), (20, 127)):
+        for t, g in ((x, dx), (w, dw)):
+            other = t.copy()
+            other[i, j] += 0.125 if other[i, j] < 0.5 else -0.125
+            diff = (loss(other, w) if t is x else loss(x, other)) - loss(x, w)
+            assert diff == (other[i, j] - t[i, j]) * g[i, j]
+
+
+def test_more_than_2_gib_of_input():
+    """Rows whose elements lie past 2^31: the quantizer's 64-bit offsets."""
+    M, N, ldx = 260, 136, 1 << 24
+    x = torch.zeros(M * ldx, dtype=torch.bfloat16, device="cuda")
+    bits = wild(M, N, 9)
+    src = torch.from_numpy(bits.view(np.int16)).cuda().view(torch.bfloat16)
+    x.view(M, ldx)[:, :N] = src
+    for layout in (T, C):
+        r, c = blob(M, N, layout), blob(N, M, layout)
+        mx.mx_quantize_fp8_b128(x, M, N, ldx, 0, None, 1, None, layout, *r, *c)
+        check_blob(r, bits, 0, 0, layout, False, "far rows")
+        check_blob(c, bits, 1, 1, layout, False, "far rows")
