@@ -70,6 +70,30 @@ __global__ __launch_bounds__(256) void quantize_f8_b128_kernel(F8QuantArgs a, ui
             v[i][0] = p[0];
             v[i][1] = p[1];
         }
+    } else if (a.ldx < (int64_t(1) << 22)) {
+        // at the edges through a range-checked buffer that ends with the tensor (in
+        // whole words, which is what the check goes by), without branches: rows past
+        // it read 0, and what lies between the rows is masked
+        const int64_t rows = a.M - r0 < kTile ? a.M - r0 : kTile;
+        const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint16_t *>(a.x + r0 * a.ldx + c0), (short)0,
+            (int)((((rows - 1) * a.ldx + (a.N - c0)) * 2 + 3) & ~int64_t(3)), 0x00020000);
+        const int left = (int)(a.N - c0 < kTile ? a.N - c0 : kTile) - 16 * tc;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int off = ((4 * tr + i) * (int)a.ldx + 16 * tc) * 2;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                v[i][h] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rx, off + 16 * h, 0, 0));
+            }
+        }
+        uint32_t keep[8];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) keep[w] = (2 * w < left ? 0x0000FFFFu : 0u) | (2 * w + 1 < left ? 0xFFFF0000u : 0u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int w = 0; w < 8; ++w) v[i][w >> 2][w & 3] &= keep[w];
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) load16(a.x, a.M, a.N, a.ldx, r0 + 4 * tr + i, c0 + 16 * tc, v[i]);
