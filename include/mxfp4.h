@@ -475,7 +475,8 @@ mx_status mx_gemm_a4w4_grouped_wgrad(int64_t M, int64_t N, int64_t K, const int3
  *     along `inner`: the row-wise grouped blobs of mx_quantize_grouped.
  *     Elements that bf16 holds as subnormal numbers may count as 0.
  *   y: tokens x K of out_dtype, stride ldy; every row is written, 0 for a token
- *     without experts.  The values of one token do not depend on the others'.
+ *     without experts.  Inf and NaN of one token reach no other; the order of a
+ *     token's fp32 sums goes by how many experts all tokens name together.
  *   workspace: mx_experts_a16w4_bytes bytes, 16-byte aligned; calls that share
  *     one must not overlap.
  * Limits: tokens <= 64, topk <= 32, experts <= 1024, x and one expert's blob below 2
