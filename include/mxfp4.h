@@ -310,7 +310,8 @@ typedef enum mx_fp8_format {
 } mx_fp8_format;
 
 /* Byte sizes of one blob (either output may be NULL).
- * Errors: MX_ERR_INVALID_ARGUMENT (negative size), MX_ERR_UNSUPPORTED (layout). */
+ * Errors: MX_ERR_INVALID_ARGUMENT (negative size), MX_ERR_UNSUPPORTED (layout,
+ * a size of 2^40 or a blob of 2^62 bytes and above). */
 mx_status mx_f8_b128_blob_bytes(int64_t rows, int64_t length, mx_layout layout, size_t *data_bytes,
                                 size_t *scale_bytes);
 

@@ -515,6 +515,11 @@ mx_status check_f8_product(const char *name, int64_t M, int64_t N, int64_t K, in
 
 mx_status mx_f8_b128_blob_bytes(int64_t rows, int64_t length, mx_layout layout, size_t *data_bytes,
                                 size_t *scale_bytes) {
+    if (rows < 0 || length < 0) return fail(MX_ERR_INVALID_ARGUMENT, "negative blob shape");
+    // (the sizes' product by division: it can pass 64 bits)
+    constexpr int64_t kMost = int64_t(1) << 40;
+    if (rows >= kMost || length >= kMost || (length > 0 && (rows + 15) > (int64_t(1) << 62) / mx::padded(length)))
+        return fail(MX_ERR_UNSUPPORTED, "a blob of %lld rows of %lld is too large", (long long)rows, (long long)length);
     MX_TRY(mx_fp8_blob_bytes(rows, length, layout, data_bytes));
     const int64_t nb = mx::cdiv(length, 128);
     if (scale_bytes)

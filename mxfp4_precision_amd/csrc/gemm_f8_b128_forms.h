@@ -16,7 +16,7 @@ enum class F8Form {
 // Whether the persistent form's epilogue takes the output: bf16, whole 16-byte
 // chunks, 32-bit offsets.
 inline bool f8_persistent_fits(const F8GemmArgs &a) {
-    return a.out_dtype == MX_BF16 && a.N % 8 == 0 && a.M * a.ldc * 2 < (int64_t(1) << 31);
+    return a.out_dtype == MX_BF16 && a.N % 8 == 0 && a.ldc <= ((int64_t(1) << 30) - 1) / a.M;
 }
 
 // Measured on MI355X in us, few rows / 128x128 / persistent / 256x256:

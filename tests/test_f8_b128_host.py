@@ -62,6 +62,10 @@ def test_blob_sizes():
     assert mx.mx_f8_b128_blob_bytes(16, 513, T) == (16 * 640, 2 * 64)
     assert mx.mx_f8_b128_blob_bytes(0, 5, T) == (0, 0) == mx.mx_f8_b128_blob_bytes(5, 0, C)
     assert status(mx.mx_f8_b128_blob_bytes, -1, 5, T) == INVALID
+    # sizes whose product passes 64 bits
+    for rows, length in ((1 << 40, 1), (1, 1 << 40), (1 << 62, 1 << 62), ((1 << 63) - 1, 5), (1 << 39, 1 << 39), (5, (1 << 63) - 1)):
+        assert status(mx.mx_f8_b128_blob_bytes, rows, length, T) == UNSUPPORTED
+        assert status(mx.mx_linear_f8_b128_bytes, rows, length) == UNSUPPORTED
     assert status(mx.mx_f8_b128_blob_bytes, 1, 5, 7) == UNSUPPORTED
 
 
