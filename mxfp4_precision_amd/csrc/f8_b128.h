@@ -20,8 +20,19 @@ template <int CTRL>
 __device__ __forceinline__ uint32_t max2_dpp(uint32_t v) {
     return max2(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
 }
-__device__ __forceinline__ uint32_t max2_xor(uint32_t v, int mask) {
-    return max2(v, (uint32_t)__shfl_xor((int)v, mask, 64));
+// Largest pattern of the lanes that differ in bit 4 (16) or 5 (32) of their
+// number: the swap of a register's odd rows with its own even ones leaves each
+// pair's values in two registers, without LDS.
+template <int MASK>
+__device__ __forceinline__ uint32_t max2_xor(uint32_t v) {
+    static_assert(MASK == 16 || MASK == 32, "");
+    if constexpr (MASK == 16) {
+        const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return max2(p[0], p[1]);
+    } else {
+        const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return max2(p[0], p[1]);
+    }
 }
 
 // Scale byte of a block from its largest bf16 magnitude: the exponent field

@@ -652,8 +652,8 @@ __device__ __forceinline__ void f8_linear_sum(const uint16_t *__restrict__ x, in
             uint32_t m = 0;
 #pragma unroll
             for (int w = 0; w < 16; ++w) m = max2(m, v[u][w >> 2][w & 3] & 0x7FFF7FFFu);
-            m = max2_xor(m, 16);
-            m = max2_xor(m, 32);
+            m = max2_xor<16>(m);
+            m = max2_xor<32>(m);
             const uint32_t c = scale_byte<FX>((m & 0xFFFFu) > (m >> 16) ? (m & 0xFFFFu) : (m >> 16));
             const float scale = scale_of(c);
             v8i aop;

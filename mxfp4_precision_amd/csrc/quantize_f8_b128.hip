@@ -122,8 +122,8 @@ __global__ __launch_bounds__(256) void quantize_f8_b128_kernel(F8QuantArgs a, ui
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
             cm[w] = max2_dpp<0x128>(cm[w]);   // lanes rotated by 8 in 16
-            cm[w] = max2_xor(cm[w], 16);
-            cm[w] = max2_xor(cm[w], 32);
+            cm[w] = max2_xor<16>(cm[w]);
+            cm[w] = max2_xor<32>(cm[w]);
         }
         if (lane < 8) {
             *reinterpret_cast<u4_t *>(&s_col[wave][8 * tc]) = u4_t{cm[0], cm[1], cm[2], cm[3]};
