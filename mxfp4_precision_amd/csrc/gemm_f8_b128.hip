@@ -380,7 +380,8 @@ __device__ __forceinline__ void f8_store_private(const v16f (&acc)[C::kMB][C::kM
             const int r = 4 * s + (lane >> 4);
             const v4u_t v = *reinterpret_cast<const v4u_t *>(slot + r * 256 + (((lane & 15) ^ (r & 15)) * 16));
             const int row = row0 + 32 * p + 4 * s;
-            const uint32_t off = row < M && col < N ? ((uint32_t)row * (uint32_t)ldc + (uint32_t)col) * 2u : kOutOfRange;
+            const uint32_t off =
+                row < M && col < N ? ((uint32_t)row * (uint32_t)ldc + (uint32_t)col) * 2u : kOutOfRange;
             __builtin_amdgcn_raw_buffer_store_b128(v, rC, off, 0, kCachePolicyNT);
         }
     }
@@ -471,41 +472,44 @@ __global__ __launch_bounds__(C::kThreads) void gemm_f8_b128_stream_kernel(int M,
 // before the sums.  Two atoms of a row group are the operand of
 // V_MFMA_SCALE_F32_16X16X128 (lane L: row L % 16, slice L / 16 of each atom; both
 // operands take their k in the same order, and the scale is the same for all
-// 128).  A workgroup's tile is MA x 16 rows x 16 NB columns; its four waves take
-// block 4 h + wave of every k-group h, so each uses one byte of the scale words
-// that all four load, and their sums are added in wave order through LDS.
-template <int FA, int FB, int MA, int NB, int DEPTH>
+// 128).  A workgroup's tile is MA x 16 rows x 16 NB columns.  Its waves split K:
+// wave w takes block w % 4 of every (WAVES / 4)-th k-group from w / 4 on, so it
+// uses one byte of each scale word, and the sums are added in wave order through
+// LDS.
+template <int FA, int FB, int MA, int NB, int WAVES, int DEPTH>
 __device__ __forceinline__ void f8_few_sum(__amdgpu_buffer_rsrc_t rA, __amdgpu_buffer_rsrc_t rAs,
                                            __amdgpu_buffer_rsrc_t rB, __amdgpu_buffer_rsrc_t rBs, int gA0, int nGA,
-                                           int gB0, int nGB, int kblocks, int kgroups, int wave, int lane,
-                                           v4f (&acc)[MA][NB], int h0 = 0) {
+                                           int gB0, int nGB, int kblocks, int kgroups, int ends, int wave,
+                                           int lane, v4f (&acc)[MA][NB], int h0 = 0) {
     int a_row[MA], b_row[NB];
 #pragma unroll
     for (int i = 0; i < MA; ++i) a_row[i] = min(gA0 + i, nGA - 1);
 #pragma unroll
     for (int j = 0; j < NB; ++j) b_row[j] = min(gB0 + j, nGB - 1);
     const uint32_t lane16 = (uint32_t)lane * 16, word = (uint32_t)(lane & 15) * 4;
-    for (; h0 + DEPTH <= kgroups; h0 += DEPTH) {
+    constexpr int kStep = WAVES / 4;
+    const int shift = 8 * (wave & 3);
+    for (; h0 + kStep * DEPTH <= ends; h0 += kStep * DEPTH) {   // ends: kgroups rounded up to whole steps
         v4u_t a[DEPTH][MA][2], b[DEPTH][NB][2];
         uint32_t as[DEPTH][MA], bs[DEPTH][NB];
 #pragma unroll
         for (int u = 0; u < DEPTH; ++u) {
-            const int h = h0 + u, kb = 4 * h + wave;
-            const bool in = kb < kblocks;   // past K: zeros (see f8_dma)
-            const uint32_t off = in ? lane16 : kOutOfRange;
+            const int h = h0 + kStep * u + (wave >> 2), kb = 4 * h + (wave & 3);
+            const bool in = kb < kblocks;   // past K: zeros, of data and scales (see f8_dma)
+            const uint32_t off = in ? lane16 : kOutOfRange, soff = in ? word : kOutOfRange;
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 const int at = in ? (b_row[j] * kblocks + kb) * 2048 : 0;
                 b[u][j][0] = __builtin_amdgcn_raw_buffer_load_b128(rB, off, at, 0);
                 b[u][j][1] = __builtin_amdgcn_raw_buffer_load_b128(rB, off + 1024, at, 0);
-                bs[u][j] = __builtin_amdgcn_raw_buffer_load_b32(rBs, word, (b_row[j] * kgroups + h) * 64, 0);
+                bs[u][j] = __builtin_amdgcn_raw_buffer_load_b32(rBs, soff, in ? (b_row[j] * kgroups + h) * 64 : 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < MA; ++i) {
                 const int at = in ? (a_row[i] * kblocks + kb) * 2048 : 0;
                 a[u][i][0] = __builtin_amdgcn_raw_buffer_load_b128(rA, off, at, 0);
                 a[u][i][1] = __builtin_amdgcn_raw_buffer_load_b128(rA, off + 1024, at, 0);
-                as[u][i] = __builtin_amdgcn_raw_buffer_load_b32(rAs, word, (a_row[i] * kgroups + h) * 64, 0);
+                as[u][i] = __builtin_amdgcn_raw_buffer_load_b32(rAs, soff, in ? (a_row[i] * kgroups + h) * 64 : 0, 0);
             }
         }
 #pragma unroll
@@ -518,32 +522,32 @@ __device__ __forceinline__ void f8_few_sum(__amdgpu_buffer_rsrc_t rA, __amdgpu_b
                                      (int)b[u][j][1][0], (int)b[u][j][1][1], (int)b[u][j][1][2], (int)b[u][j][1][3]};
                     const v8i aop = {(int)a[u][i][0][0], (int)a[u][i][0][1], (int)a[u][i][0][2], (int)a[u][i][0][3],
                                      (int)a[u][i][1][0], (int)a[u][i][1][1], (int)a[u][i][1][2], (int)a[u][i][1][3]};
-                    const int sb = (int)(bs[u][j] >> (8 * wave)), sa = (int)(as[u][i] >> (8 * wave));
+                    const int sb = (int)(bs[u][j] >> shift), sa = (int)(as[u][i] >> shift);
                     const v4f cin = acc[i][j];
                     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bop, aop, cin, FB, FA, 0, sb, 0, sa);
                 }
     }
     if constexpr (DEPTH > 1)
-        f8_few_sum<FA, FB, MA, NB, DEPTH / 2>(rA, rAs, rB, rBs, gA0, nGA, gB0, nGB, kblocks, kgroups, wave, lane, acc,
-                                              h0);
+        f8_few_sum<FA, FB, MA, NB, WAVES, DEPTH / 2>(rA, rAs, rB, rBs, gA0, nGA, gB0, nGB, kblocks, kgroups, ends, wave,
+                                                     lane, acc, h0);
 }
 
-// The four waves' sums, added in wave order and stored: lane L of tile (i, j)
+// The waves' sums, added in wave order and stored: lane L of tile (i, j)
 // holds row 16 i + L % 16, columns 16 j + 4 (L / 16) + 0..3.
-template <int MA, int NB, bool OUT_BF16>
+template <int MA, int NB, int WAVES, bool OUT_BF16>
 __device__ __forceinline__ void f8_few_store(const v4f (&acc)[MA][NB], int64_t row0, int64_t col0, int64_t M,
                                              int64_t N, const uint16_t *bias, void *Cout, int64_t ldc, int wave,
                                              int lane) {
-    __shared__ v4f s_sum[4][MA * NB][64];
+    __shared__ v4f s_sum[WAVES][MA * NB][64];
 #pragma unroll
     for (int i = 0; i < MA; ++i)
 #pragma unroll
         for (int j = 0; j < NB; ++j) s_sum[wave][i * NB + j][lane] = acc[i][j];
     __syncthreads();
-    for (int t = wave; t < MA * NB; t += 4) {
+    for (int t = wave; t < MA * NB; t += WAVES) {
         v4f v = s_sum[0][t][lane];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) {
+        for (int w = 1; w < WAVES; ++w) {
             const v4f q = s_sum[w][t][lane];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] += q[e];
@@ -580,14 +584,11 @@ __device__ __forceinline__ void f8_few_store(const v4f (&acc)[MA][NB], int64_t r
     }
 }
 
-template <int FA, int FB, int MA, int NB, bool OUT_BF16>
-__global__ __launch_bounds__(256) void gemm_f8_b128_few_kernel(int64_t M, int64_t N, int kblocks, int tiles_n,
-                                                               const uint8_t *__restrict__ A,
-                                                               const uint8_t *__restrict__ As,
-                                                               const uint8_t *__restrict__ B,
-                                                               const uint8_t *__restrict__ Bs,
-                                                               const uint16_t *__restrict__ bias,
-                                                               void *__restrict__ Cout, int64_t ldc) {
+template <int FA, int FB, int MA, int NB, int WAVES, bool OUT_BF16>
+__global__ __launch_bounds__(64 * WAVES) void gemm_f8_b128_few_kernel(
+    int64_t M, int64_t N, int kblocks, int tiles_n, const uint8_t *__restrict__ A, const uint8_t *__restrict__ As,
+    const uint8_t *__restrict__ B, const uint8_t *__restrict__ Bs, const uint16_t *__restrict__ bias,
+    void *__restrict__ Cout, int64_t ldc) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tn = blockIdx.x % tiles_n, tm = blockIdx.x / tiles_n;
@@ -597,42 +598,52 @@ __global__ __launch_bounds__(256) void gemm_f8_b128_few_kernel(int64_t M, int64_
     for (int i = 0; i < MA; ++i)
 #pragma unroll
         for (int j = 0; j < NB; ++j) acc[i][j] = v4f{};
-    f8_few_sum<FA, FB, MA, NB, MA * NB >= 4 ? 2 : 8 / (MA * NB)>(
+    f8_few_sum<FA, FB, MA, NB, WAVES, MA * NB >= 4 ? 2 : 8 / (MA * NB)>(
         make_rsrc(A, (int64_t)nGA * kblocks * 2048), make_rsrc(As, (int64_t)nGA * kgroups * 64),
         make_rsrc(B, (int64_t)nGB * kblocks * 2048), make_rsrc(Bs, (int64_t)nGB * kgroups * 64), tm * MA, nGA,
-        tn * NB, nGB, kblocks, kgroups, wave, lane, acc);
-    f8_few_store<MA, NB, OUT_BF16>(acc, (int64_t)tm * MA * 16, (int64_t)tn * NB * 16, M, N, bias, Cout, ldc, wave,
-                                   lane);
+        tn * NB, nGB, kblocks, kgroups, (kgroups + WAVES / 4 - 1) / (WAVES / 4) * (WAVES / 4), wave, lane, acc);
+    f8_few_store<MA, NB, WAVES, OUT_BF16>(acc, (int64_t)tm * MA * 16, (int64_t)tn * NB * 16, M, N, bias, Cout, ldc,
+                                          wave, lane);
 }
 
 // A linear layer on up to 16 rows in one launch: as the few-rows product, but a
 // wave quantizes the blocks of x that it multiplies.  Lane L holds row L % 16's
 // slice L / 16 of both halves of a block, so the block's maximum is a lane
 // exchange away and the codes are the operand; every workgroup does so for itself
-// (x is small and stays in the L2s), while its weights are on their way.
+// (x is small and stays in the L2s), while its weights are on their way.  Eight
+// waves split K: wave w takes block w % 4 of every other k-group from w / 4 on, two
+// at a time.  In us, 4 waves with four in flight / 8 with two / 16 with two: 1 row
+// 4096 x 4096 7.1 / 5.9 / 5.8, 16 rows 9.5 / 7.8 / 7.8, 1 row 1024 x 1024 3.0 / 2.9
+// / 4.0.
+constexpr int kLinearWaves = 8;
 template <int FX, int FW, int DEPTH>
 __device__ __forceinline__ void f8_linear_sum(const uint16_t *__restrict__ x, int64_t M, int64_t K, int64_t ldx,
                                               __amdgpu_buffer_rsrc_t rB, __amdgpu_buffer_rsrc_t rBs, int g,
-                                              int kblocks, int kgroups, int wave, int lane, v4f &acc, int h0 = 0) {
+                                              int kblocks, int kgroups, int ends, int wave, int lane, v4f &acc,
+                                              int h0 = 0) {
     const uint32_t lane16 = (uint32_t)lane * 16, word = (uint32_t)(lane & 15) * 4;
     const int64_t r = lane & 15;
-    for (; h0 + DEPTH <= kgroups; h0 += DEPTH) {
+    constexpr int kStep = kLinearWaves / 4;
+    const int shift = 8 * (wave & 3);
+    for (; h0 + kStep * DEPTH <= ends; h0 += kStep * DEPTH) {   // ends: kgroups rounded up to whole steps
         v4u_t b[DEPTH][2];
         uint32_t bs[DEPTH];
         u4_t v[DEPTH][4];
 #pragma unroll
         for (int u = 0; u < DEPTH; ++u) {
-            const int h = h0 + u, kb = 4 * h + wave;
-            const bool in = kb < kblocks;   // past K: zeros (see f8_dma)
+            const int h = h0 + kStep * u + (wave >> 2), kb = 4 * h + (wave & 3);
+            const bool in = kb < kblocks;   // past K: zeros, of data and scales (see f8_dma)
             const uint32_t off = in ? lane16 : kOutOfRange;
             const int at = in ? (g * kblocks + kb) * 2048 : 0;
             b[u][0] = __builtin_amdgcn_raw_buffer_load_b128(rB, off, at, 0);
             b[u][1] = __builtin_amdgcn_raw_buffer_load_b128(rB, off + 1024, at, 0);
-            bs[u] = __builtin_amdgcn_raw_buffer_load_b32(rBs, word, (g * kgroups + h) * 64, 0);
+            bs[u] = __builtin_amdgcn_raw_buffer_load_b32(rBs, in ? word : kOutOfRange,
+                                                           in ? (g * kgroups + h) * 64 : 0, 0);
         }
 #pragma unroll
         for (int u = 0; u < DEPTH; ++u) {
-            const int64_t k0 = 128 * (int64_t)(4 * (h0 + u) + wave), k = k0 + 16 * (lane >> 4);
+            const int64_t k0 = 128 * (int64_t)(4 * (h0 + kStep * u + (wave >> 2)) + (wave & 3));
+            const int64_t k = k0 + 16 * (lane >> 4);
             if (k0 + 128 <= K) {
 #pragma unroll
                 for (int w = 0; w < 4; ++w) v[u][w] = u4_t{};
@@ -664,30 +675,29 @@ __device__ __forceinline__ void f8_linear_sum(const uint16_t *__restrict__ x, in
             }
             const v8i bop = {(int)b[u][0][0], (int)b[u][0][1], (int)b[u][0][2], (int)b[u][0][3],
                              (int)b[u][1][0], (int)b[u][1][1], (int)b[u][1][2], (int)b[u][1][3]};
-            const int sb = (int)(bs[u] >> (8 * wave)), sa = (int)c;
+            const int sb = (int)(bs[u] >> shift), sa = (int)c;
             const v4f cin = acc;
             acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bop, aop, cin, FW, FX, 0, sb, 0, sa);
         }
     }
     if constexpr (DEPTH > 1)
-        f8_linear_sum<FX, FW, DEPTH / 2>(x, M, K, ldx, rB, rBs, g, kblocks, kgroups, wave, lane, acc, h0);
+        f8_linear_sum<FX, FW, DEPTH / 2>(x, M, K, ldx, rB, rBs, g, kblocks, kgroups, ends, wave, lane, acc, h0);
 }
 
 template <int FX, int FW, bool OUT_BF16>
-__global__ __launch_bounds__(256) void linear_f8_b128_kernel(int64_t M, int64_t N, int64_t K,
-                                                             const uint16_t *__restrict__ x, int64_t ldx,
-                                                             const uint8_t *__restrict__ W,
-                                                             const uint8_t *__restrict__ Ws,
-                                                             const uint16_t *__restrict__ bias, void *__restrict__ y,
-                                                             int64_t ldy) {
+__global__ __launch_bounds__(64 * kLinearWaves) void linear_f8_b128_kernel(
+    int64_t M, int64_t N, int64_t K, const uint16_t *__restrict__ x, int64_t ldx, const uint8_t *__restrict__ W,
+    const uint8_t *__restrict__ Ws, const uint16_t *__restrict__ bias, void *__restrict__ y, int64_t ldy) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kblocks = (int)cdiv(K, 128), kgroups = (kblocks + 3) / 4, nGB = (int)cdiv(N, 16);
     const int gB0 = (int)blockIdx.x;
     v4f acc[1][1] = {};
-    f8_linear_sum<FX, FW, 4>(x, M, K, ldx, make_rsrc(W, (int64_t)nGB * kblocks * 2048),
-                             make_rsrc(Ws, (int64_t)nGB * kgroups * 64), gB0, kblocks, kgroups, wave, lane, acc[0][0]);
-    f8_few_store<1, 1, OUT_BF16>(acc, 0, 16 * (int64_t)gB0, M, N, bias, y, ldy, wave, lane);
+    f8_linear_sum<FX, FW, 2>(x, M, K, ldx, make_rsrc(W, (int64_t)nGB * kblocks * 2048),
+                             make_rsrc(Ws, (int64_t)nGB * kgroups * 64), gB0, kblocks, kgroups,
+                             (kgroups + kLinearWaves / 4 - 1) / (kLinearWaves / 4) * (kLinearWaves / 4), wave, lane,
+                             acc[0][0]);
+    f8_few_store<1, 1, kLinearWaves, OUT_BF16>(acc, 0, 16 * (int64_t)gB0, M, N, bias, y, ldy, wave, lane);
 }
 
 template <int FX, int FW>
@@ -695,8 +705,8 @@ hipError_t launch_linear(const F8LinearArgs &a, hipStream_t stream) {
     const F8GemmArgs &g = a.g;
     const bool bf = g.out_dtype == MX_BF16;
     auto kernel = bf ? linear_f8_b128_kernel<FX, FW, true> : linear_f8_b128_kernel<FX, FW, false>;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)cdiv(g.N, 16)), dim3(256), 0, stream, g.M, g.N, g.K, a.x, a.ldx, g.B,
-                       g.Bs, g.bias, g.C, g.ldc);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)cdiv(g.N, 16)), dim3(64 * kLinearWaves), 0, stream, g.M, g.N, g.K, a.x,
+                       a.ldx, g.B, g.Bs, g.bias, g.C, g.ldc);
     return hipGetLastError();
 }
 
@@ -724,11 +734,20 @@ hipError_t launch_formats(const F8GemmArgs &a, hipStream_t stream) {
             const int ma = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
             const int nb = ma == 1 ? 1 : 2;
             const int64_t tiles_n = cdiv(a.N, 16 * nb), tiles = cdiv(a.M, 16 * ma) * tiles_n;
-            auto kernel = ma == 1   ? gemm_f8_b128_few_kernel<FA, FB, 1, 1, OUT_BF16>
-                          : ma == 2 ? gemm_f8_b128_few_kernel<FA, FB, 2, 2, OUT_BF16>
-                                    : gemm_f8_b128_few_kernel<FA, FB, 4, 2, OUT_BF16>;
-            hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(256), 0, stream, a.M, a.N, (int)(K_pad / 128),
-                               (int)tiles_n, a.A, a.As, a.B, a.Bs, a.bias, a.C, a.ldc);
+            // Eight waves for the widest tile where no CU gets two of them (us, 4 waves /
+            // 8: 64 x 4096 x 4096 8.7 / 7.3, 512 x 1024 x 8192 14.9 / 11.6, 333 x 712 x
+            // 1000 4.8 / 4.6; with three tiles a CU, of which it then holds one at a time,
+            // 333 x 4096 x 4096 15.1 / 18.6).  With one k-group half of them would idle
+            // (712 x 1000 x 328 4.2 / 6.1), and for the small tiles four do as well (16 x
+            // 4096 x 4096 5.0 / 5.25, 23 x 5000 x 2888 5.9 / 6.0, 32 x 4096 x 4096 6.5 /
+            // 6.1).
+            const bool wide = ma == 4 && K_pad > 512 && tiles <= device_cu_count();
+            auto kernel = ma == 1   ? gemm_f8_b128_few_kernel<FA, FB, 1, 1, 4, OUT_BF16>
+                          : ma == 2 ? gemm_f8_b128_few_kernel<FA, FB, 2, 2, 4, OUT_BF16>
+                          : wide    ? gemm_f8_b128_few_kernel<FA, FB, 4, 2, 8, OUT_BF16>
+                                    : gemm_f8_b128_few_kernel<FA, FB, 4, 2, 4, OUT_BF16>;
+            hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(wide ? 512 : 256), 0, stream, a.M, a.N,
+                               (int)(K_pad / 128), (int)tiles_n, a.A, a.As, a.B, a.Bs, a.bias, a.C, a.ldc);
             break;
         }
         case F8Form::kTiles128: {

@@ -43,7 +43,7 @@ inline F8Form f8_gemm_form(const F8GemmArgs &a, int cus) {
 }
 
 // Whether a linear layer of M rows quantizes x inside the product.  In us, one
-// launch / two: 1 row, 4096 x 4096 7.7 / 10.9; 23 rows (two row tiles), 5003 x
+// launch / two: 1 row, 4096 x 4096 5.9 / 10; 23 rows (two row tiles), 5003 x
 // 2889 14.1 / 11.7, as every workgroup reads and quantizes all of x.
 inline bool f8_linear_fused(int64_t M) { return M <= 16; }
 
