@@ -466,7 +466,8 @@ mx_status mx_gemm_a4w4_grouped_wgrad(int64_t M, int64_t N, int64_t K, const int3
  * A whole layer of gated experts for a few tokens (decoding), two launches:
  *   y_t = sum_j w_tj * D_e (silu(G_e x_t) * (U_e x_t)),   e = ids[t][j]
  * with bf16 activations on the experts' MXFP4 weights, fp32 sums; silu(v) =
- * v / (1 + exp(-v)), the product with U_e x_t rounded to bf16 before D_e.
+ * v / (1 + exp(-v)), the product with U_e x_t held as the sum of two bf16 (to 2^-16
+ * of it) before D_e.
  *   x: tokens x K bf16, stride ldx.  ids: device int32, tokens x topk; an id
  *     outside [0, experts) counts nothing (an expert that lives elsewhere), one
  *     that a token names more than once counts with the sum of its weights.

@@ -771,7 +771,7 @@ struct ExpertSpace {
 };
 ExpertSpace expert_space(int64_t tokens, int64_t inner, int topk) {
     return {mx::kExpertSplits * sizeof(int), (size_t)tokens * mx::kExpertSplits * 16 * sizeof(float),
-            (size_t)(mx::expert_tiles(tokens * topk) * 16 * mx::padded(inner)) * 2};
+            (size_t)(mx::expert_tiles(tokens * topk) * 16 * mx::padded(inner)) * 4};
 }
 
 }  // namespace

@@ -15,11 +15,19 @@
 // L 32 codes of row L % 16, and the words j of the four lanes of a row are the
 // operand of the j-th of four MFMAs, k = 32 (L / 16) + 8 j + 0..7.  The activations
 // between the products are written in the order in which the second reads them, a
-// column tile of 16 tokens of an expert as 1 KB for each MFMA.
+// column tile of 16 tokens of an expert as 1 KB for each MFMA, each as the sum of
+// two bf16.
 //
 // Sums do not depend on timing: waves split k (up) or the experts' atoms (down)
 // and are added in order in LDS; where a row tile of `down` is split over
 // workgroups, each writes its sums and the last one to finish adds all in order.
+//
+// Bound by reading the weights, or by latency where they are few.  Measured on
+// MI355X, the two kernels in us: 1 token, 8 of 64 experts, 2048 x 1024 7.6 + 7.7;
+// 16 tokens, 4 of 32, 4096 x 1536 28 + 24 (6.3 and 3.6 TB/s); 64 tokens, 8 of 64,
+// 2048 x 1024 32 + 35.  (With activations of one bf16 `down` reads half as much of
+// them from the L2s, 7.0, 17 and 25 us, but the outputs' error grows from 0.0017 to
+// 0.0024 and more.)
 
 #include <type_traits>
 
@@ -151,7 +159,8 @@ __device__ __forceinline__ RowAt row_at(int row, int ksteps, int kgroups, int la
 // c lies at p ^ c % 16, so that both sides touch all banks.
 template <int RT, int MT, int DEPTH>
 __device__ __forceinline__ void up_sum(__amdgpu_buffer_rsrc_t rW, __amdgpu_buffer_rsrc_t rS,
-                                       const RowAt (&row)[2][RT], __amdgpu_buffer_rsrc_t rX, const uint32_t (&x)[MT * 4], int n, uint8_t *lds,
+                                       const RowAt (&row)[2][RT], __amdgpu_buffer_rsrc_t rX,
+                                       const uint32_t (&x)[MT * 4], int n, uint8_t *lds,
                                        int K, int ksteps, int kgroups, int wave, int lane, v4f (&acc)[2][RT][MT],
                                        int h0 = 0) {
     for (; h0 + DEPTH <= kgroups; h0 += DEPTH) {
@@ -275,11 +284,20 @@ __device__ __forceinline__ void up_tile(const ExpertsArgs &a, v4f *s_sum, uint8_
         float h[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) h[q] = i + q < inner ? g[q] / (1.0f + expf(-g[q])) * u[q] : 0.0f;
-        // bf16, the type of the next product's operand: off by at most 2^-8 of each, as every activation held in bf16;
-        // in the order of that operand: atom i / 128, MFMA i / 8 % 4, lane of the column and of i / 32 % 4
-        uint16_t *at = a.h + ((int64_t)(to + m) * (padded(a.inner) / 128) + i / 128) * 2048 + (i / 8 % 4) * 512 +
+        // For the next product as the sum of two bf16, off by at most 2^-8 of the second, that is 2^-16 of h (one bf16
+        // would add an error as large as the output's own rounding).  In the order of its operands: atom i / 128, MFMA
+        // i / 8 % 4, lane of the column and of i / 32 % 4; the second bf16 behind the atom's first.
+        uint16_t *at = a.h + ((int64_t)(to + m) * (padded(a.inner) / 128) + i / 128) * 4096 + (i / 8 % 4) * 512 +
                        ((lane & 15) + 16 * (i / 32 % 4)) * 8 + i % 8;
-        *reinterpret_cast<u2_t *>(at) = u2_t{pack(h[0], h[1]), pack(h[2], h[3])};
+        const u2_t hi = {pack(h[0], h[1]), pack(h[2], h[3])};
+        float rest[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float r = __uint_as_float(q & 1 ? hi[q >> 1] & 0xFFFF0000u : hi[q >> 1] << 16);
+            rest[q] = __builtin_isfinite(r) ? h[q] - r : 0.0f;
+        }
+        *reinterpret_cast<u2_t *>(at + 2048) = u2_t{pack(rest[0], rest[1]), pack(rest[2], rest[3])};
+        *reinterpret_cast<u2_t *>(at) = hi;
     }
 }
 
@@ -295,7 +313,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void experts_up_kernel(ExpertsArgs a
         for (int i = threadIdx.x; i < kExpertSplits; i += 64 * kUpWaves) a.counters[i] = 0;
     read_routing(r, a, ids, 64 * kUpWaves);
     if (slot >= r.count) return;
-    const int e = __builtin_amdgcn_readfirstlane((int)r.list[slot]), to = __builtin_amdgcn_readfirstlane((int)r.tile[slot]);
+    const int e = __builtin_amdgcn_readfirstlane((int)r.list[slot]);
+    const int to = __builtin_amdgcn_readfirstlane((int)r.tile[slot]);
     const uint64_t mask = tokens_of(a, ids, e, lane);
     const int n = __popcll(mask);
     uint8_t *lds = s_dynamic + wave * kUpTiles * 4096;
@@ -315,7 +334,7 @@ template <int MT, int DEPTH>
 __device__ __forceinline__ void down_sum(__amdgpu_buffer_rsrc_t rW, __amdgpu_buffer_rsrc_t rS, RowAt row,
                                          const uint16_t *const (&h)[MT], int c, int end, v4f (&acc)[MT]) {
     for (; c + DEPTH <= end; c += DEPTH) {
-        u4_t w[DEPTH], v[DEPTH][MT][4];
+        u4_t w[DEPTH], v[DEPTH][MT][8];
         uint32_t s[DEPTH];
 #pragma unroll
         for (int u = 0; u < DEPTH; ++u) {
@@ -327,8 +346,8 @@ __device__ __forceinline__ void down_sum(__amdgpu_buffer_rsrc_t rW, __amdgpu_buf
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    v[u][m][j] = *reinterpret_cast<const u4_t *>(h[m] + (int64_t)(c + u) * 2048 + j * 512);
+                for (int j = 0; j < 8; ++j)
+                    v[u][m][j] = *reinterpret_cast<const u4_t *>(h[m] + (int64_t)(c + u) * 4096 + j * 512);
 #pragma unroll
         for (int u = 0; u < DEPTH; ++u) {
             const float scale = scale_of((s[u] >> (8 * ((c + u) & 3))) & 0xFFu);
@@ -337,8 +356,10 @@ __device__ __forceinline__ void down_sum(__amdgpu_buffer_rsrc_t rW, __amdgpu_buf
                 const bf8_t a = weights8(w[u][j], scale);
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
-                    acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf8_t, v[u][m][j]), acc[m],
-                                                                     0, 0, 0);
+#pragma unroll
+                    for (int part = 0; part < 8; part += 4)
+                        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            a, __builtin_bit_cast(bf8_t, v[u][m][part + j]), acc[m], 0, 0, 0);
             }
         }
     }
@@ -348,8 +369,8 @@ __device__ __forceinline__ void down_sum(__amdgpu_buffer_rsrc_t rW, __amdgpu_buf
 // Adds an expert's part, for its columns [first, first + 16 MT) in column tiles
 // `from` on, to the wave's sums of all tokens, s_sum[token][row].
 template <int MT>
-__device__ __forceinline__ void down_part(const ExpertsArgs &a, const int *ids, const float *weights, float *s_sum, int e, uint64_t mask,
-                                          int first, int from, int n0, int c0, int c1, int lane) {
+__device__ __forceinline__ void down_part(const ExpertsArgs &a, const int *ids, const float *weights, float *s_sum, int e,
+                                          uint64_t mask, int first, int from, int n0, int c0, int c1, int lane) {
     const int ksteps = (int)(padded(a.inner) / 128), kgroups = (ksteps + 3) / 4, n = __popcll(mask) - first;
     const int64_t groups = cdiv(a.K, 16), bytes = groups * ksteps * 1024, sbytes = groups * kgroups * 256;
     const uint16_t *h[MT];
@@ -357,7 +378,7 @@ __device__ __forceinline__ void down_part(const ExpertsArgs &a, const int *ids, 
     for (int m = 0; m < MT; ++m) {
         // (columns past the expert's tokens: its last one again, not added)
         const int c = min(lane & 15, max(n - 16 * m, 1) - 1);
-        h[m] = a.h + (int64_t)(16 * m < n ? from + m : from) * ksteps * 2048 + (c + (lane & 48)) * 8;
+        h[m] = a.h + (int64_t)(16 * m < n ? from + m : from) * ksteps * 4096 + (c + (lane & 48)) * 8;
     }
     v4f acc[MT];
 #pragma unroll

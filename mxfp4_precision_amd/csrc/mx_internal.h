@@ -92,7 +92,7 @@ struct ExpertsArgs {
     void *y;
     int *counters;              // kExpertSplits, zeroed by the first kernel
     float *sums;                // kExpertSplits x 16 x tokens
-    uint16_t *h;                // expert_tiles x 16 x padded(inner) activations
+    uint16_t *h;                // expert_tiles x 16 x padded(inner) activations, two bf16 each
 };
 // Column tiles of 16 tokens that pairs can make: one for each expert that they
 // name, and one more for every 16.

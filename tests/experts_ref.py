@@ -12,7 +12,8 @@ def experts(x, ids, weights, w1, w2):
     """(y, bar): x [t, K], ids and weights [t, topk], w1 [E, 2 inner, K], w2 [E, K, inner], all 64-bit values.
 
     What the kernels round: sums in fp32 (of n products in any order: at most n 2^-24 of the sum of their magnitudes),
-    the activations to bf16 (8 significant bits: half a step is at most 2^-8 of a value in [1, 2), that is of 1; silu and its product in fp32 add 2^-21 at most), products and sums in fp32
+    the activations to the sum of two bf16 (8 significant bits: the first is off by at most half a step, 2^-8 of the
+    value, the second by 2^-8 of that; silu and its product in fp32 add 2^-21 at most), products and sums in fp32
     again."""
     T, K = x.shape
     inner = w2.shape[2]
@@ -31,10 +32,11 @@ def experts(x, ids, weights, w1, w2):
             h = g * sig * u
             # |d silu / dg| <= 1.1
             dh = 1.1 * err[:inner] * np.abs(u) + np.abs(g * sig) * err[inner:] + 1.1 * err[:inner] * err[inner:]
-            dh += (2.0 ** -8 + 2.0 ** -21) * (np.abs(h) + dh) + 2.0 ** -134
+            dh += (2.0 ** -16 + 2.0 ** -21) * (np.abs(h) + dh) + 2.0 ** -134
             part = np.abs(w2[e]) @ (np.abs(h) + dh)
             w = abs(weights[t, j])
             y[t] += weights[t, j] * (w2[e] @ h)
-            bar[t] += w * (np.abs(w2[e]) @ dh + (inner + 8) * 2.0 ** -24 * part)
+            # (2 inner products, of both halves, whose magnitudes add up to 1 + 2^-7 of h at most)
+            bar[t] += w * (np.abs(w2[e]) @ dh + (2 * inner + 8) * 2.0 ** -24 * part * (1 + 2.0 ** -7))
             bar[t] += (E + ids.shape[1] + 16) * 2.0 ** -24 * w * part
     return y, bar
