@@ -104,7 +104,8 @@ inline int64_t expert_tiles(int64_t pairs) { return (pairs < kExpertsMost ? pair
 inline int expert_row_tiles(int pairs, int slots) { return pairs >= 4 * slots ? 2 : 1; }
 // Workgroups that share a row tile of the down product: 1.5 workgroups per CU
 // (64 tokens, 8 of 64 experts, 2048 x 1024, 128 row tiles: 2, 3, 4 and 8 of them
-// 33, 29, 31 and 37 us; 16 tokens, 256 row tiles: 1, 3 and 4 18, 22 and 24 us),
+// 33, 29, 31 and 37 us; 16 tokens, 256 row tiles: 1, 3 and 4 18, 22 and 24 us, both
+// measured with activations of one bf16),
 // each with four atoms for each of its 8 waves at least.
 inline int expert_splits(int slots, int64_t tiles, int64_t inner) {
     const int64_t atoms = slots * (padded(inner) / 128);
