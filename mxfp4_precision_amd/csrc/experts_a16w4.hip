@@ -23,11 +23,11 @@
 // workgroups, each writes its sums and the last one to finish adds all in order.
 //
 // Bound by reading the weights, or by latency where they are few.  Measured on
-// MI355X, the two kernels in us: 1 token, 8 of 64 experts, 2048 x 1024 7.6 + 7.7;
-// 16 tokens, 4 of 32, 4096 x 1536 28 + 24 (6.3 and 3.6 TB/s); 64 tokens, 8 of 64,
-// 2048 x 1024 32 + 35.  (With activations of one bf16 `down` reads half as much of
-// them from the L2s, 7.0, 17 and 25 us, but the outputs' error grows from 0.0017 to
-// 0.0024 and more.)
+// MI355X, the two kernels in us: 1 token, 8 of 64 experts, 2048 x 1024 7.6 + 6.6;
+// 16 tokens, 4 of 32, 4096 x 1536 28 + 19 (6.3 and 4.7 TB/s); 64 tokens, 8 of 64,
+// 2048 x 1024 32 + 32.  Of an expert with up to 8 tokens `down` takes both bf16 in
+// one column tile (without: 7.6, 24 and 35 us).  With activations of one bf16 it
+// takes 7.0, 17 and 25, but the outputs' error grows from 0.0017 to 0.0024 and more.
 
 #include <type_traits>
 
@@ -329,12 +329,14 @@ __global__ __launch_bounds__(64 * kUpWaves) void experts_up_kernel(ExpertsArgs a
 }
 
 // Sums of a wave over atoms c .. end - 1 of one expert's `down`; h: the lane's
-// operands of atom 0, a column tile every `stride` of them.
-template <int MT, int DEPTH>
+// operands of atom 0, a column tile every `stride` of them.  PARTS: 8, both bf16
+// of the activations one after the other, or 4, where columns 8 to 15 hold the
+// second ones.
+template <int MT, int PARTS, int DEPTH>
 __device__ __forceinline__ void down_sum(__amdgpu_buffer_rsrc_t rW, __amdgpu_buffer_rsrc_t rS, RowAt row,
                                          const uint16_t *const (&h)[MT], int c, int end, v4f (&acc)[MT]) {
     for (; c + DEPTH <= end; c += DEPTH) {
-        u4_t w[DEPTH], v[DEPTH][MT][8];
+        u4_t w[DEPTH], v[DEPTH][MT][PARTS];
         uint32_t s[DEPTH];
 #pragma unroll
         for (int u = 0; u < DEPTH; ++u) {
@@ -346,7 +348,7 @@ __device__ __forceinline__ void down_sum(__amdgpu_buffer_rsrc_t rW, __amdgpu_buf
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < PARTS; ++j)
                     v[u][m][j] = *reinterpret_cast<const u4_t *>(h[m] + (int64_t)(c + u) * 4096 + j * 512);
 #pragma unroll
         for (int u = 0; u < DEPTH; ++u) {
@@ -357,18 +359,19 @@ __device__ __forceinline__ void down_sum(__amdgpu_buffer_rsrc_t rW, __amdgpu_buf
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int part = 0; part < 8; part += 4)
+                    for (int part = 0; part < PARTS; part += 4)
                         acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                             a, __builtin_bit_cast(bf8_t, v[u][m][part + j]), acc[m], 0, 0, 0);
             }
         }
     }
-    if constexpr (DEPTH > 1) down_sum<MT, DEPTH / 2>(rW, rS, row, h, c, end, acc);
+    if constexpr (DEPTH > 1) down_sum<MT, PARTS, DEPTH / 2>(rW, rS, row, h, c, end, acc);
 }
 
 // Adds an expert's part, for its columns [first, first + 16 MT) in column tiles
-// `from` on, to the wave's sums of all tokens, s_sum[token][row].
-template <int MT>
+// `from` on, to the wave's sums of all tokens, s_sum[token][row].  PAIR: for up to
+// 8 columns.
+template <int MT, bool PAIR>
 __device__ __forceinline__ void down_part(const ExpertsArgs &a, const int *ids, const float *weights, float *s_sum, int e,
                                           uint64_t mask, int first, int from, int n0, int c0, int c1, int lane) {
     const int ksteps = (int)(padded(a.inner) / 128), kgroups = (ksteps + 3) / 4, n = __popcll(mask) - first;
@@ -377,14 +380,18 @@ __device__ __forceinline__ void down_part(const ExpertsArgs &a, const int *ids, 
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         // (columns past the expert's tokens: its last one again, not added)
-        const int c = min(lane & 15, max(n - 16 * m, 1) - 1);
-        h[m] = a.h + (int64_t)(16 * m < n ? from + m : from) * ksteps * 4096 + (c + (lane & 48)) * 8;
+        const int c = min(lane & (PAIR ? 7 : 15), max(n - 16 * m, 1) - 1);
+        h[m] = a.h + (int64_t)(16 * m < n ? from + m : from) * ksteps * 4096 + (c + (lane & 48)) * 8 +
+               (PAIR && (lane & 8) ? 2048 : 0);
     }
     v4f acc[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[m] = v4f{};
-    down_sum<MT, 4 / MT>(make_rsrc(a.W2 + e * bytes, bytes), make_rsrc(a.W2s + e * sbytes, sbytes),
+    down_sum<MT, PAIR ? 4 : 8, 4 / MT>(make_rsrc(a.W2 + e * bytes, bytes), make_rsrc(a.W2s + e * sbytes, sbytes),
                          row_at(n0 + (lane & 15), ksteps, kgroups, lane), h, c0, c1, acc);
+    if constexpr (PAIR)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[0][q] += __shfl_xor(acc[0][q], 8, 64);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         const int c = 16 * m + (lane & 15);
@@ -448,11 +455,13 @@ __global__ __launch_bounds__(64 * kDownWaves) void experts_down_kernel(ExpertsAr
         const int from = __builtin_amdgcn_readfirstlane((int)r.tile[slot]);
         const uint64_t mask = tokens_of(a, ids, e, lane);
         const int n = __popcll(mask);
-        if (n <= 16) {
-            down_part<1>(a, ids, weights, own, e, mask, 0, from, n0, c0, c1, lane);
+        if (n <= 8) {
+            down_part<1, true>(a, ids, weights, own, e, mask, 0, from, n0, c0, c1, lane);
+        } else if (n <= 16) {
+            down_part<1, false>(a, ids, weights, own, e, mask, 0, from, n0, c0, c1, lane);
         } else {
             for (int first = 0; first < n; first += 32)
-                down_part<2>(a, ids, weights, own, e, mask, first, from + first / 16, n0, c0, c1, lane);
+                down_part<2, false>(a, ids, weights, own, e, mask, first, from + first / 16, n0, c0, c1, lane);
         }
         at += c1 - c0;
     }
