@@ -481,9 +481,10 @@ mx_status mx_gemm_a4w4_grouped_wgrad(int64_t M, int64_t N, int64_t K, const int3
  *     token's fp32 sums goes by how many experts all tokens name together.
  *   workspace: mx_experts_a16w4_bytes bytes, 16-byte aligned; calls that share
  *     one must not overlap.
- * Limits: tokens <= 64, topk <= 32, experts <= 1024, x and one expert's blob below 2
- * GiB; for more tokens the grouped calls above.  tokens == 0 or K == 0 is a
- * no-op; topk == 0 or inner == 0 writes zeros.
+ * Limits: tokens <= 64, topk <= 32, experts <= 1024, K and inner below 2^24,
+ * cdiv(inner,128) * experts below 2^21, x from its first to its last element and one
+ * expert's blob below 2 GiB; for more tokens the grouped calls above.  tokens == 0 or
+ * K == 0 is a no-op; topk == 0 or inner == 0 writes zeros.
  * Requires x, y, W1, W2, their scales and the workspace 16-byte aligned, ids and
  * weights 4-byte aligned, ldx % 8 == 0 and ldy % 8 == 0.
  * Errors: INVALID_ARGUMENT, MISALIGNED, UNSUPPORTED (layout, out_dtype, sizes),

@@ -811,7 +811,8 @@ mx_status mx_experts_a16w4(int64_t tokens, int64_t K, int64_t inner, int experts
     if ((reinterpret_cast<uintptr_t>(ids) & 3u) || (reinterpret_cast<uintptr_t>(weights) & 3u))
         return fail(MX_ERR_MISALIGNED, "ids and weights must be 4-byte aligned");
     if (ldy % 8) return fail(MX_ERR_MISALIGNED, "ldy=%lld must be a multiple of 8", (long long)ldy);
-    if (ldx >= (int64_t(1) << 24) || ((tokens - 1) * ldx + K) * 2 >= (int64_t(1) << 31) - 4)
+    // (by division: the product can pass 64 bits)
+    if (tokens > 1 && ldx > ((int64_t(1) << 30) - 3 - K) / (tokens - 1))
         return fail(MX_ERR_UNSUPPORTED, "%s: x spans 2 GiB or more", name);
     // (a grid of 256-thread workgroups must stay below 2^32 threads)
     if ((int64_t)experts * (mx::padded(inner) / 16) >= (int64_t(1) << 24))
