@@ -505,7 +505,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void experts_down_kernel(ExpertsAr
 hipError_t launch_experts(const ExpertsArgs &a, mx_dtype out_dtype, hipStream_t stream) {
     const int pairs = a.tokens * a.topk, slots = a.experts < pairs ? a.experts : pairs;
     if (slots > 0) {
-        const int rows = expert_row_tiles(pairs, slots), tiles = (int)(padded(a.inner) / (16 * rows));
+        const int rows = expert_row_tiles(slots, a.inner), tiles = (int)(padded(a.inner) / (16 * rows));
         auto kernel = rows == 2 ? experts_up_kernel<2> : experts_up_kernel<1>;
         hipLaunchKernelGGL(kernel, dim3((unsigned)(slots * tiles)), dim3(64 * kUpWaves),
                            (unsigned)(kUpWaves * kUpTiles * 4096 + pairs * 4), stream, a, tiles);

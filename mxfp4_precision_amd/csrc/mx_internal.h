@@ -97,11 +97,17 @@ struct ExpertsArgs {
 // Column tiles of 16 tokens that pairs can make: one for each expert that they
 // name, and one more for every 16.
 inline int64_t expert_tiles(int64_t pairs) { return (pairs < kExpertsMost ? pairs : kExpertsMost) + pairs / 16; }
-// Tiles of 16 rows of the up product that a workgroup takes: two where an expert
-// can have 4 tokens on average, which halves the reading of activations.  In us,
-// one / two: 64 tokens, 8 of 64 experts, 2048 x 1024 38 / 32; 16 tokens, 4 of 32,
-// 4096 x 1536 28.6 / 27.5; 5 tokens 5.9 / 7.1, 1 token 7.5 / 9.2.
-inline int expert_row_tiles(int pairs, int slots) { return pairs >= 4 * slots ? 2 : 1; }
+// Tiles of 16 rows of the up product that a workgroup takes.  Two halve the reading
+// of activations and the workgroups that find out the routing, but need 4 workgroups
+// of one tile for each CU, for all experts that the pairs can name.  In us a call,
+// one / two, after that number of workgroups: 360 (5 tokens, 2 of 9, 1001 x 523)
+// 12.9 / 13.9; 512 (1 token, 8 of 64, 2048 x 1024 17.9 / 19.4; 64 tokens, 8 of 8,
+// 2048 x 1024 40.7 / 44.2); 768 (3 tokens, 4 of 64, 2048 x 1024) 20.1 / 22.1; 1024 (2
+// tokens, 8 of 64, 2048 x 1024 25.9 / 25.2; 1 token, 1 of 8, 4096 x 16384 33.0 / 31.1;
+// 2 tokens, 2 of 8, 2048 x 4096 23.2 / 24.2); 4096 (64 tokens, 8 of 64, 2048 x 1024)
+// 87.5 / 81.3; 5888 (16 tokens, 4 of 32, 2880 x 2880) 79.6 / 74.4; 8192 (64 tokens, 8
+// of 256, 1024 x 512) 65.6 / 53.0.
+inline int expert_row_tiles(int slots, int64_t inner) { return slots * (padded(inner) / 16) >= 1024 ? 2 : 1; }
 // Workgroups that share a row tile of the down product: 1.5 workgroups per CU
 // (64 tokens, 8 of 64 experts, 2048 x 1024, 128 row tiles: 2, 3, 4 and 8 of them
 // 33, 29, 31 and 37 us; 16 tokens, 256 row tiles: 1, 3 and 4 18, 22 and 24 us, both

@@ -66,6 +66,18 @@ def test_the_steps_of_the_list(layer):
             lay.check(x, ids, w, "border %d" % border)
 
 
+@pytest.mark.parametrize("E,topk,K,inner", [(9, 2, 1001, 523), (40, 2, 1001, 523), (70, 2, 1, 255), (64, 2, 2049, 257),
+                                            (8, 8, 40, 2049)])
+def test_odd_sizes_in_one_and_two_row_tiles(oracle_mod, E, topk, K, inner):
+    """Workgroups of the up product that take 16 rows or 32, with one and with two column tiles."""
+    lay = Layer(oracle_mod, E, K, inner)
+    for t in (2, 40):
+        ids, w = routing(t, E, topk, t)
+        lay.check(tokens(t, K), ids, w, "%d tokens" % t)
+        ids[:, 0] = E - 1
+        lay.check(tokens(t, K), ids, w, "%d tokens of one expert" % t)
+
+
 def test_rows_far_apart(layer):
     """Two rows of x that lie 1 GiB apart, and one with a stride past 32 bits."""
     lay = layer(64)
