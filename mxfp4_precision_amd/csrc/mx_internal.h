@@ -81,7 +81,7 @@ struct F8LinearArgs {
 
 // A layer of experts for a few tokens.
 constexpr int kExpertTokens = 64, kExpertTopk = 32, kExpertsMost = 1024;
-constexpr int kExpertSplits = 384;   // most workgroups of the down product where it is split
+constexpr int kExpertSplits = 256;   // most workgroups of the down product where it is split
 struct ExpertsArgs {
     int tokens, experts, topk;
     int64_t K, inner, ldx, ldy;
@@ -108,11 +108,15 @@ inline int64_t expert_tiles(int64_t pairs) { return (pairs < kExpertsMost ? pair
 // 87.5 / 81.3; 5888 (16 tokens, 4 of 32, 2880 x 2880) 79.6 / 74.4; 8192 (64 tokens, 8
 // of 256, 1024 x 512) 65.6 / 53.0.
 inline int expert_row_tiles(int slots, int64_t inner) { return slots * (padded(inner) / 16) >= 1024 ? 2 : 1; }
-// Workgroups that share a row tile of the down product: 1.5 workgroups per CU
-// (64 tokens, 8 of 64 experts, 2048 x 1024, 128 row tiles: 2, 3, 4 and 8 of them
-// 33, 29, 31 and 37 us; 16 tokens, 256 row tiles: 1, 3 and 4 18, 22 and 24 us, both
-// measured with activations of one bf16),
-// each with four atoms for each of its 8 waves at least.
+// Workgroups that share a row tile of the down product: one workgroup per CU in all,
+// each with four atoms for each of its 8 waves at least.  In us a call, one per CU /
+// 1.5: 160 row tiles (K 2560, inner 768), 64 tokens, 8 of 128 110.5 / 110.5, 8 tokens
+// 40.1 / 41.2; 128 (2048 x 1024, 8 of 64), 64 tokens 77.4 / 81.3, 16 tokens 43.5 /
+// 46.5, 2 tokens 24.9 / 25.9; 96 (1536 x 1024, 6 of 64), 16 tokens 36.3 / 36.3; 64
+// (1024 x 4096, 4 of 16), 64 tokens 70.3 / 72.3; 48 (768 x 2048, 4 of 16), 8 tokens
+// 23.4 / 24.7; 32 (512 x 4096, 2 of 8), 8 tokens 20.8 / 22.4, with half as many as one
+// per CU 19.8.  Not split at all, 128 row tiles: 64 tokens 93.7, 1 token 17.1 against
+// 17.6.
 inline int expert_splits(int slots, int64_t tiles, int64_t inner) {
     const int64_t atoms = slots * (padded(inner) / 128);
     int64_t n = atoms / 32;

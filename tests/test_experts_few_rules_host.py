@@ -38,3 +38,16 @@ def test_row_tiles(tmp_path):
            (1, 1, 1, 64, 16257), (64, 32, 128, 64, 1), (64, 32, 1024, 64, 4096)]
     got = rules(tmp_path, one + two)
     assert [(c, r) for c, (r, _) in zip(one + two, got) if r != (1 if c in one else 2)] == []
+
+
+def test_splits(tmp_path):
+    """The down product's row tiles are shared by as many workgroups as make one for each of 256 CUs at most, and by no
+    more than have 32 atoms of weights each."""
+    cases = {(64, 8, 64, 2048, 1024): 2, (16, 8, 64, 2048, 1024): 2, (2, 8, 64, 2048, 1024): 2, (64, 8, 128, 2560, 768): 1,
+             (8, 8, 128, 2560, 768): 1, (64, 4, 32, 2880, 2880): 1, (64, 6, 64, 1536, 1024): 2, (64, 4, 16, 1024, 4096): 4,
+             (8, 4, 16, 768, 2048): 5, (8, 2, 8, 512, 4096): 8, (16, 4, 32, 4096, 1536): 1, (64, 32, 1024, 16, 16384): 256,
+             # few atoms
+             (1, 8, 64, 2048, 1024): 2, (1, 1, 8, 64, 128): 1, (5, 2, 9, 1001, 523): 1, (1, 1, 1, 64, 8064): 1,
+             (1, 1, 1, 64, 8065): 2, (1, 0, 4, 64, 1024): 1, (3, 2, 4, 64, 0): 1}
+    got = rules(tmp_path, list(cases))
+    assert [(c, s) for (c, want), (_, s) in zip(cases.items(), got) if s != want] == []

@@ -78,6 +78,17 @@ def test_odd_sizes_in_one_and_two_row_tiles(oracle_mod, E, topk, K, inner):
         lay.check(tokens(t, K), ids, w, "%d tokens of one expert" % t)
 
 
+@pytest.mark.parametrize("E,topk,K,inner", [(64, 4, 24, 4096), (64, 32, 16, 2000), (30, 4, 120, 1100)])
+def test_many_parts_of_a_row_tile(oracle_mod, E, topk, K, inner):
+    """Row tiles of the down product that 64, 32 and 8 workgroups share, with 64 tokens; five times the same."""
+    lay = Layer(oracle_mod, E, K, inner)
+    ids, w = routing(64, E, topk)
+    x = tokens(64, K)
+    first = lay.check(x, ids, w, "%d x %d" % (K, inner))
+    for _ in range(5):
+        assert torch.equal(lay.run(x, ids, w), first)
+
+
 def test_rows_far_apart(layer):
     """Two rows of x that lie 1 GiB apart, and one with a stride past 32 bits."""
     lay = layer(64)
