@@ -622,7 +622,7 @@ mx_status mx_grad_norm_bytes(int64_t count, size_t *bytes);
  * norm alone.  Tensors with numel == 0 are skipped; without elements the norm
  * is 0.  workspace: mx_grad_norm_bytes(count) bytes, 8-byte aligned; calls that
  * share it, or info, must not overlap.
- * Requires gradients 16-byte aligned.
+ * Requires gradients 16-byte aligned, info and step 8-byte aligned.
  * Errors: MX_ERR_INVALID_ARGUMENT (NULL, count < 0, numel < 0, max_norm < 0 or
  * NaN, grad_scale < 0 or not finite in fp32), MX_ERR_MISALIGNED, MX_ERR_UNSUPPORTED (a dtype,
  * numel above 2^33, count above 2^20), MX_ERR_DEVICE_UNSUPPORTED, MX_ERR_HIP.

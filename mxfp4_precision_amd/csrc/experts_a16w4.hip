@@ -22,12 +22,18 @@
 // and are added in order in LDS; where a row tile of `down` is split over
 // workgroups, each writes its sums and the last one to finish adds all in order.
 //
-// Bound by reading the weights, or by latency where they are few.  Measured on
-// MI355X, the two kernels in us: 1 token, 8 of 64 experts, 2048 x 1024 7.6 + 6.6;
-// 16 tokens, 4 of 32, 4096 x 1536 28 + 19 (6.3 and 4.7 TB/s); 64 tokens, 8 of 64,
-// 2048 x 1024 32 + 32.  Of an expert with up to 8 tokens `down` takes both bf16 in
-// one column tile (without: 7.6, 24 and 35 us).  With activations of one bf16 it
-// takes 7.0, 17 and 25, but the outputs' error grows from 0.0017 to 0.0024 and more.
+// An expert with more than 32 tokens is done in runs of 32, each of which reads its
+// weights again.
+//
+// Bound by latency where the weights are few, else by how many loads are in flight
+// (the first kernel: two atoms a wave, three workgroups a CU for their LDS) and by
+// the activations, which the second reads from L2 once for every 16 rows of W2, 4
+// to 8 KB for each KB of weights.  Measured on MI355X, the two kernels in us, two
+// sets of inputs in turn: 1 token, 8 of 64 experts, 2048 x 1024 8.8 + 8.2; 16 tokens,
+// 4 of 32, 4096 x 1536 (17 experts named, 114 + 57 MB) 30 + 23, 3.8 and 2.4 TB/s; 64
+// tokens, 8 of 64, 2048 x 1024 (48 named, 107 + 53 MB) 38 + 40, 2.8 and 1.3 TB/s.
+// With activations of one bf16 the outputs' error grows from 0.0017 to 0.0024 and
+// more.
 
 #include <type_traits>
 
